@@ -17,9 +17,19 @@ and "Edge order is explicit"), with A_w[dst_e, src_e] = w_e:
     ag_step(g, w, X, dY)         -> (Y, dX, dw): forward and fused backward in one call, overlapped
     ag_step_host(g, w, X, dY, ...)  the three from host buffers, copies included
     ag_step_host_pipelined(...)     the same for back-to-back steps (copies overlap across steps)
+
+A differential attention layer around the same graphs:
+
+    ag_rotary(Q, K, pos, inv_freq, heads)     rotary positions ahead of the scores (ag_rotary_freqs: the table)
+    ag_diff_attn_fwd(g, Q, K, V, lam, scale)  Y = sum of (alpha_1 - lambda alpha_2) V per destination row, with dropout
+    ag_diff_attn_backward(...)                its gradients
+    ag_resnorm_fwd(R, B, G, ...)              norm, gate, dropout, residual sum and the next norm in one pass
+    ag_resnorm_backward(...)                  their gradients
+    ag_dropout(X, p, seed, offset)            dropout of features or edge weights, the mask never stored
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -28,6 +38,8 @@ import torch
 
 __all__ = ["AggraphError", "Graph", "ag_graph_lower", "ag_spmm_fwd", "ag_spmm_dx", "ag_sddmm_dw", "ag_backward",
            "ag_mean_fwd", "ag_mean_backward", "ag_gcn_norm", "ag_attn_fwd", "ag_attn_backward", "ag_step",
+           "ag_diff_attn_fwd", "ag_diff_attn_backward", "ag_dropout", "ag_rotary", "ag_rotary_freqs",
+           "ag_resnorm_fwd", "ag_resnorm_backward",
            "ag_step_host", "ag_step_host_pipelined", "ag_step_staging_bytes", "ag_graph_workspace_bytes", "lib", "LIB_PATH",
            "declared_symbols", "AG_F32", "AG_BF16"]
 
@@ -63,6 +75,12 @@ class Stats(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class ResNorm(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("gamma1", "beta1", "scale", "gamma2", "beta2")] + [
+        ("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("eps", ctypes.c_float),
+        ("norm", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 _P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
@@ -101,6 +119,18 @@ def _bind(handle: ctypes.CDLL) -> ctypes.CDLL:
     handle.ag_step_scratch_bytes.argtypes = [_P, _I64]
     handle.ag_step_scratch_bytes.restype = _SZ
     handle.ag_step.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I64, _I, _P, _SZ, _P]
+    _F, _D, _U64 = ctypes.c_float, ctypes.c_double, ctypes.c_uint64
+    handle.ag_dropout.argtypes = [_P, _P, _I64, _D, _U64, _U64, _I, _P]
+    handle.ag_rotary.argtypes = [_P] * 6 + [_I64] * 4 + [_I, _F, _I, _I, _P]
+    handle.ag_rotary_freqs.argtypes = [_I64, _D, _I, _D, _D, _D, _D, _P, _P]
+    handle.ag_diff_attn_scratch_bytes.argtypes = [_P, _I64, _I64]
+    handle.ag_diff_attn_scratch_bytes.restype = _SZ
+    handle.ag_diff_attn_fwd.argtypes = [_P] * 5 + [_F, _D, _U64, _U64, _P, _P, _I64, _I64, _I, _P, _SZ, _P]
+    handle.ag_diff_attn_backward.argtypes = [_P] * 5 + [_F, _D, _U64, _U64] + [_P] * 6 + [_I64, _I64, _I, _P, _SZ, _P]
+    handle.ag_resnorm_fwd.argtypes = [ctypes.POINTER(ResNorm)] + [_P] * 5 + [_I64, _I64, _I, _P]
+    handle.ag_resnorm_scratch_bytes.argtypes = [_I64, _I64]
+    handle.ag_resnorm_scratch_bytes.restype = _SZ
+    handle.ag_resnorm_backward.argtypes = [ctypes.POINTER(ResNorm)] + [_P] * 13 + [_I64, _I64, _I, _P, _SZ, _P]
     handle.ag_graph_free.argtypes = [_P]
     handle.ag_graph_free.restype = None
     handle.ag_last_error.restype = ctypes.c_char_p
@@ -109,7 +139,9 @@ def _bind(handle: ctypes.CDLL) -> ctypes.CDLL:
     for name in ("ag_graph_lower", "ag_graph_arrays", "ag_graph_get_stats", "ag_spmm_fwd", "ag_spmm_dx",
                  "ag_sddmm_dw", "ag_backward", "ag_step", "ag_spmm_fwd_static_scratch", "ag_step_host",
                  "ag_step_host_pipelined", "ag_abi_version",
-                 "ag_mean_fwd", "ag_mean_backward", "ag_gcn_norm", "ag_attn_fwd", "ag_attn_backward"):
+                 "ag_mean_fwd", "ag_mean_backward", "ag_gcn_norm", "ag_attn_fwd", "ag_attn_backward",
+                 "ag_dropout", "ag_rotary", "ag_rotary_freqs", "ag_diff_attn_fwd", "ag_diff_attn_backward",
+                 "ag_resnorm_fwd", "ag_resnorm_backward"):
         getattr(handle, name).restype = _I
     return handle
 
@@ -463,6 +495,233 @@ def ag_attn_backward(g: Graph, Q, K, V, scale: float, alpha, dY, dQ=None, dK=Non
                                 _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), H, code, _ptr(scr), scr.numel(),
                                 _stream(g.device, stream)))
     return tuple(outs)
+
+
+@contextlib.contextmanager
+def _allocating_on(device: torch.device, stream):
+    """Tensors made inside belong to the stream that the call runs on, so that
+    their memory is not handed out again while the call's work is pending."""
+    if stream is None:
+        yield
+        return
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        yield
+
+
+def _u64(name: str, v: int) -> int:
+    v = int(v)
+    if not 0 <= v < 1 << 64:
+        raise AggraphError(1, f"{name} must be in [0, 2^64)")
+    return v
+
+
+def _like(name: str, t, of: torch.Tensor) -> torch.Tensor:
+    """The output tensor `t`, checked against `of` (a new one where None)."""
+    if t is None:
+        return torch.empty_like(of)
+    _need_cuda(name, t)
+    if t.shape != of.shape or t.dtype != of.dtype:
+        raise AggraphError(2, f"{name} must have shape {tuple(of.shape)} and dtype {of.dtype}")
+    return t
+
+
+def _vector(name: str, t, n: int) -> torch.Tensor:
+    _need_cuda(name, t)
+    if t.dtype != torch.float32:
+        raise AggraphError(3, f"{name} must be float32")
+    if tuple(t.shape) != (n,):
+        raise AggraphError(2, f"{name} must be [{n}], got {tuple(t.shape)}")
+    return t
+
+
+def ag_dropout(X: torch.Tensor, p: float, seed: int, offset: int = 0, out=None, stream=None) -> torch.Tensor:
+    """X / (1 - p) where kept, else 0: element i (of the flat array) by word i % 4 of the
+    Philox4x32-10 block (i / 4, offset) under key `seed`.  The gradient is the same call on dY."""
+    _need_cuda("X", X)
+    code = _dtype_code(X)
+    with _allocating_on(X.device, stream):
+        out = _like("out", out, X)
+    _check(lib.ag_dropout(_ptr(X), _ptr(out), X.numel(), float(p), _u64("seed", seed), _u64("offset", offset), code,
+                          _stream(X.device, stream)))
+    return out
+
+
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def ag_rotary_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                    original: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq, factor) for ag_rotary: a float64 host tensor [rot / 2] and the outputs' factor."""
+    if scaling not in _SCALINGS:
+        raise AggraphError(1, f"unknown scaling {scaling!r}; expected one of {tuple(_SCALINGS)}")
+    inv_freq = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    out = ctypes.c_double()
+    _check(lib.ag_rotary_freqs(int(rot), float(base), _SCALINGS[scaling], float(factor), float(original),
+                               float(beta_fast), float(beta_slow), _ptr(inv_freq), ctypes.byref(out)))
+    return inv_freq, out.value
+
+
+def ag_rotary(Q: torch.Tensor, K, pos: torch.Tensor, inv_freq: torch.Tensor, heads: int, interleaved=False,
+              factor: float = 1.0, inverse=False, Qo=None, Ko=None, stream=None):
+    """(Qo, Ko): the first 2 * len(inv_freq) columns of every head rotated by pos * inv_freq
+    (K may be None).  inverse=True is the gradient.  Outputs may be the inputs."""
+    _need_cuda("Q", Q)
+    if Q.dim() != 2:
+        raise AggraphError(2, f"Q must be [N, H], got {tuple(Q.shape)}")
+    code = _dtype_code(Q)
+    N, H = Q.shape
+    for name, t, dtype, n in (("pos", pos, torch.int64, N), ("inv_freq", inv_freq, torch.float64, None)):
+        _need_cuda(name, t)
+        if t.dtype != dtype:
+            raise AggraphError(3, f"{name} must be {dtype}")
+        if t.dim() != 1 or (n is not None and t.shape[0] != n):
+            raise AggraphError(2, f"{name} must be one-dimensional{'' if n is None else f' of length {n}'}")
+    if K is not None:
+        _like("K", K, Q)
+    elif Ko is not None:
+        raise AggraphError(1, "Ko without K")
+    with _allocating_on(Q.device, stream):
+        Qo = _like("Qo", Qo, Q)
+        Ko = None if K is None else _like("Ko", Ko, K)
+    _check(lib.ag_rotary(_ptr(Q), _ptr(K), _ptr(pos), _ptr(inv_freq), _ptr(Qo), _ptr(Ko), N, H, int(heads),
+                         2 * inv_freq.shape[0], int(bool(interleaved)), float(factor), int(bool(inverse)), code,
+                         _stream(Q.device, stream)))
+    return Qo, Ko
+
+
+def ag_diff_attn_fwd(g: Graph, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lam: torch.Tensor, scale: float,
+                     p: float = 0.0, seed: int = 0, offset: int = 0, Y=None, lse=None, stream=None):
+    """Differential edge-softmax attention of len(lam) heads: (Y, lse) with
+    Y = sum over edges of u (alpha_1 - lam alpha_2) V and lse [N, heads, 2]."""
+    code = _same_feats(g, ("Q", "K", "V"), (Q, K, V))
+    _need_cuda("lam", lam)
+    heads = _vector("lam", lam, lam.numel()).shape[0]
+    H = Q.shape[1]
+    n = int(lib.ag_diff_attn_scratch_bytes(g.handle, H, heads))
+    if n == 0:
+        raise AggraphError(2, f"H = {H} is not 2 * heads * d with heads = {heads} in [1, 256] and d in [1, 256]")
+    with _allocating_on(g.device, stream):
+        Y = _like("Y", Y, V)
+        if lse is None:
+            lse = torch.empty((g.N, heads, 2), dtype=torch.float32, device=g.device)
+        else:
+            _check_lse(g, lse, heads)
+        scr = torch.empty(n, dtype=torch.uint8, device=g.device)
+    _check(lib.ag_diff_attn_fwd(g.handle, _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), float(scale), float(p),
+                                _u64("seed", seed), _u64("offset", offset), _ptr(Y), _ptr(lse), H, heads, code,
+                                _ptr(scr), n, _stream(g.device, stream)))
+    return Y, lse
+
+
+def _check_lse(g: Graph, lse: torch.Tensor, heads: int) -> None:
+    _need_cuda("lse", lse)
+    if lse.dtype != torch.float32:
+        raise AggraphError(3, "lse must be float32")
+    if tuple(lse.shape) != (g.N, heads, 2):
+        raise AggraphError(2, f"lse must be [{g.N}, {heads}, 2], got {tuple(lse.shape)}")
+
+
+def ag_diff_attn_backward(g: Graph, Q, K, V, lam, scale: float, lse, dY, p: float = 0.0, seed: int = 0,
+                          offset: int = 0, dQ=None, dK=None, dV=None, dlam=None, stream=None):
+    """Gradients (dQ, dK, dV, dlam) of ag_diff_attn_fwd for the upstream gradient dY (p, seed
+    and offset as in the forward call, lse from it)."""
+    code = _same_feats(g, ("Q", "K", "V", "dY"), (Q, K, V, dY))
+    _need_cuda("lam", lam)
+    heads = _vector("lam", lam, lam.numel()).shape[0]
+    H = Q.shape[1]
+    n = int(lib.ag_diff_attn_scratch_bytes(g.handle, H, heads))
+    if n == 0:
+        raise AggraphError(2, f"H = {H} is not 2 * heads * d with heads = {heads} in [1, 256] and d in [1, 256]")
+    _check_lse(g, lse, heads)
+    with _allocating_on(g.device, stream):
+        dQ, dK, dV = _like("dQ", dQ, Q), _like("dK", dK, K), _like("dV", dV, V)
+        dlam = torch.empty_like(lam) if dlam is None else _vector("dlam", dlam, heads)
+        scr = torch.empty(n, dtype=torch.uint8, device=g.device)
+    _check(lib.ag_diff_attn_backward(g.handle, _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), float(scale), float(p),
+                                     _u64("seed", seed), _u64("offset", offset), _ptr(lse), _ptr(dY), _ptr(dQ),
+                                     _ptr(dK), _ptr(dV), _ptr(dlam), H, heads, code, _ptr(scr), n,
+                                     _stream(g.device, stream)))
+    return dQ, dK, dV, dlam
+
+
+_NORMS = {"rms": 0, "layer": 1}
+_ACTS = {"sigmoid": 0, "silu": 1}
+
+
+def _resnorm_op(H, gamma1, beta1, scale, gamma2, beta2, eps, norm, act, p, seed, offset) -> ResNorm:
+    if norm not in _NORMS or act not in _ACTS:
+        raise AggraphError(1, f"unknown norm {norm!r} or gate {act!r}; expected one of {tuple(_NORMS)}, {tuple(_ACTS)}")
+    ptrs = []
+    for name, t in (("gamma1", gamma1), ("beta1", beta1), ("scale", scale), ("gamma2", gamma2), ("beta2", beta2)):
+        ptrs.append(None if t is None else _vector(name, t, H).data_ptr())
+    return ResNorm(*ptrs, float(p), _u64("seed", seed), _u64("offset", offset), float(eps), _NORMS[norm], _ACTS[act])
+
+
+def _resnorm_rows(named):
+    """(first tensor, dtype code) of the [N, H] matrices that are given, all alike."""
+    given = [(name, t) for name, t in named if t is not None]
+    if not given:
+        raise AggraphError(1, "no matrix given")
+    first = given[0][1]
+    _need_cuda(given[0][0], first)
+    if first.dim() != 2:
+        raise AggraphError(2, f"{given[0][0]} must be [N, H], got {tuple(first.shape)}")
+    for name, t in given[1:]:
+        _like(name, t, first)
+    return first, _dtype_code(first)
+
+
+def ag_resnorm_fwd(R, B, G=None, gamma1=None, beta1=None, scale=None, gamma2=None, beta2=None, eps: float = 1e-5,
+                   norm: str = "rms", act: str = "sigmoid", p: float = 0.0, seed: int = 0, offset: int = 0,
+                   next_norm: bool = True, X=None, Z=None, stream=None):
+    """(X, Z): X = R + scale * drop(act(G) * (norm(B) gamma1 + beta1)) and Z = norm(X) gamma2 + beta2.
+    Without B, X is R itself and Z its norm; next_norm=False leaves Z out (None)."""
+    first, code = _resnorm_rows((("R", R), ("B", B), ("G", G)))
+    op = _resnorm_op(first.shape[1], gamma1, beta1, scale, gamma2, beta2, eps, norm, act, p, seed, offset)
+    if B is None and X is not None:
+        raise AggraphError(1, "X without a block output (the sum is R)")
+    if not next_norm and Z is not None:
+        raise AggraphError(1, "Z without the next norm")
+    with _allocating_on(first.device, stream):
+        X = None if B is None else _like("X", X, first)
+        Z = _like("Z", Z, first) if next_norm else None
+    _check(lib.ag_resnorm_fwd(ctypes.byref(op), _ptr(R), _ptr(B), _ptr(G), _ptr(X), _ptr(Z), first.shape[0],
+                              first.shape[1], code, _stream(first.device, stream)))
+    return (R if B is None else X), Z
+
+
+def ag_resnorm_backward(X, B, G, dX, dZ, gamma1=None, beta1=None, scale=None, gamma2=None, beta2=None,
+                        eps: float = 1e-5, norm: str = "rms", act: str = "sigmoid", p: float = 0.0, seed: int = 0,
+                        offset: int = 0, stream=None) -> dict:
+    """Gradients of ag_resnorm_fwd for dX and dZ (either may be None) from the stored sum X: a dict
+    of "R" (the sum's gradient), "B", "G" and, for every vector that is given, "gamma1", "beta1",
+    "scale", "gamma2", "beta2" (float32 [H])."""
+    first, code = _resnorm_rows((("X", X), ("B", B), ("G", G), ("dX", dX), ("dZ", dZ)))
+    N, H = first.shape
+    op = _resnorm_op(H, gamma1, beta1, scale, gamma2, beta2, eps, norm, act, p, seed, offset)
+    vectors = {"gamma1": gamma1, "beta1": beta1, "scale": scale, "gamma2": gamma2, "beta2": beta2}
+    if B is None and any(t is not None for t in (gamma1, beta1, scale)):
+        raise AggraphError(1, "a vector of the block's norm without its output B")
+    if dZ is None and (gamma2 is not None or beta2 is not None):
+        raise AggraphError(1, "a vector of the next norm without dZ")
+    with _allocating_on(first.device, stream):
+        out = {"R": torch.empty_like(first)}
+        if B is not None:
+            out["B"] = torch.empty_like(first)
+        if G is not None:
+            out["G"] = torch.empty_like(first)
+        n = 0
+        if any(t is not None for t in vectors.values()):
+            n = int(lib.ag_resnorm_scratch_bytes(N, H))
+            for name, t in vectors.items():
+                if t is not None:
+                    out[name] = torch.empty_like(t)
+        scr = torch.empty(n, dtype=torch.uint8, device=first.device) if n else None
+    _check(lib.ag_resnorm_backward(ctypes.byref(op), _ptr(X), _ptr(B), _ptr(G), _ptr(dX), _ptr(dZ),
+                                   *[_ptr(out.get(k)) for k in ("R", "B", "G")], *[_ptr(out.get(k)) for k in vectors],
+                                   N, H, code, _ptr(scr), n, _stream(first.device, stream)))
+    return out
 
 
 def ag_spmm_fwd_static_scratch(g: Graph, w: torch.Tensor, X: torch.Tensor, out=None, stream=None) -> torch.Tensor:

@@ -1,0 +1,837 @@
+// Row-wise operators around an attention layer: dropout, rotary positions and
+// the norm / gate / residual block with its gradients.  Each makes one pass
+// over its matrices and is bound by HBM; none needs a graph.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "aggraph.h"
+#include "frag.cuh"
+#include "internal.h"
+#include "random.cuh"
+
+namespace ag {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kSMs = 148;
+
+// ---------------------------------------------------------------------------- dropout
+
+// y_i = keep_i x_i / (1 - p).  A thread takes VEC (a multiple of 4)
+// consecutive elements per step: VEC / 4 Philox blocks.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) k_dropout(const T *__restrict__ x, T *__restrict__ y, int64_t n, const Drop drop) {
+    using F = Frag<T, VEC>;
+    const int64_t vecs = n / VEC;
+    const int64_t stride = int64_t(gridDim.x) * blockDim.x;
+    const int64_t i0 = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    for (int64_t i = i0; i < vecs; i += stride) {
+        const typename F::raw r = F::load_stream(x + i * VEC);
+        float v[VEC];
+        F::unpack(r, v);
+#pragma unroll
+        for (int q = 0; q < VEC / 4; ++q) {
+            const uint32_t k = keep4(uint64_t(i) * (VEC / 4) + q, drop);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * q + j] = k >> j & 1u ? v[4 * q + j] * drop.scale : 0.f;
+        }
+        F::store(y + i * VEC, v);
+    }
+    // the last n % VEC elements
+    const int64_t i = vecs * VEC + i0;
+    if (i < n) {
+        float v[1];
+        Frag<T, 1>::unpack(Frag<T, 1>::load_stream(x + i), v);
+        v[0] = keep4(uint64_t(i) >> 2, drop) >> (i & 3) & 1u ? v[0] * drop.scale : 0.f;
+        Frag<T, 1>::store(y + i, v);
+    }
+}
+// Addresses without a vector: four elements per block one by one.
+template <typename T>
+__global__ void __launch_bounds__(256) k_dropout_scalar(const T *__restrict__ x, T *__restrict__ y, int64_t n,
+                                                        const Drop drop) {
+    const int64_t stride = int64_t(gridDim.x) * blockDim.x;
+    for (int64_t b = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; b * 4 < n; b += stride) {
+        const uint32_t k = keep4(uint64_t(b), drop);
+        for (int j = 0; j < 4 && b * 4 + j < n; ++j) {
+            float v[1];
+            Frag<T, 1>::unpack(Frag<T, 1>::load_stream(x + b * 4 + j), v);
+            v[0] = k >> j & 1u ? v[0] * drop.scale : 0.f;
+            Frag<T, 1>::store(y + b * 4 + j, v);
+        }
+    }
+}
+
+unsigned grid_of(int64_t work, int64_t per_block, int64_t most) {
+    const int64_t b = (work + per_block - 1) / per_block;
+    return unsigned(b < 1 ? 1 : (b > most ? most : b));
+}
+
+template <typename T, int VEC>
+void launch_dropout(const void *X, void *Y, int64_t n, const Drop &drop, cudaStream_t st) {
+    const T *x = static_cast<const T *>(X);
+    T *y = static_cast<T *>(Y);
+    if ((uintptr_t(X) | uintptr_t(Y)) % (VEC * sizeof(T)) == 0)
+        k_dropout<T, VEC><<<grid_of(n / VEC + 1, 256, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
+    else
+        k_dropout_scalar<T><<<grid_of((n + 3) / 4, 256, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
+}
+
+// ---------------------------------------------------------------------------- rotary positions
+
+// Pair i of a head (i < rot / 2) is rotated by the angle pos[n] inv_freq[i]
+// and scaled by `factor`; the columns from rot on are copied.  The angle is
+// reduced in turns in fp64 (an fp32 angle at position 2^20 is off by 0.03),
+// then one fp32 sincospi.  A block takes `rows` rows: it computes their
+// rot / 2 angles once into shared memory, for all heads of both matrices.
+struct RotaryParams {
+    const void *in[2];
+    void *out[2];
+    const int64_t *pos;
+    const double *inv_freq;
+    int64_t N;
+    int mats, H, D, rot, heads, rows;
+    float factor, sign;
+};
+
+constexpr int kMaxRot = 4096;
+
+template <typename T, int VEC, bool HALF>
+__global__ void __launch_bounds__(256) k_rotary(const RotaryParams P) {
+    extern __shared__ float2 turn[];  // [rows][rot / 2]: factor * (cos, sin)
+    using F = Frag<T, VEC>;
+    const int64_t n0 = int64_t(blockIdx.x) * P.rows;
+    const int rows = int(P.N - n0 < P.rows ? P.N - n0 : P.rows);
+    const int pairs = P.rot / 2;
+    for (int i = threadIdx.x; i < rows * pairs; i += blockDim.x) {
+        const int r = i / pairs;
+        const double u = double(P.pos[n0 + r]) * (P.inv_freq[i - r * pairs] * 0.15915494309189535);  // turns
+        float s, c;
+        sincospif(float(2.0 * (u - rint(u))), &s, &c);
+        turn[i] = make_float2(P.factor * c, P.sign * P.factor * s);
+    }
+    __syncthreads();
+    // units of a head: rotated (two vectors, or one with both halves of its pairs), then copied vectors
+    constexpr bool kPairInVec = !HALF && VEC > 1;
+    const int rot_units = kPairInVec ? P.rot / VEC : pairs / VEC;
+    const int head_units = rot_units + (P.D - P.rot) / VEC;
+    const int row_units = head_units * P.heads;
+    const int total = rows * row_units * P.mats;
+    for (int i = threadIdx.x; i < total; i += blockDim.x) {
+        const int mat = i >= rows * row_units;
+        const int k = i - mat * rows * row_units;
+        const int r = k / row_units;
+        const int q = k - r * row_units;
+        const int head = q / head_units;
+        const int u = q - head * head_units;
+        const int64_t base = (n0 + r) * P.H + int64_t(head) * P.D;
+        const T *x = static_cast<const T *>(mat ? P.in[1] : P.in[0]) + base;
+        T *y = static_cast<T *>(mat ? P.out[1] : P.out[0]) + base;
+        const float2 *cs = turn + r * pairs;
+        float a[VEC], b[VEC];
+        if (u >= rot_units) {
+            const int at = P.rot + (u - rot_units) * VEC;
+            F::unpack(F::load_stream(x + at), a);
+            F::store(y + at, a);
+        } else if (kPairInVec) {
+            F::unpack(F::load_stream(x + u * VEC), a);
+#pragma unroll
+            for (int v = 0; v + 1 < VEC; v += 2) {
+                const float2 t = cs[(u * VEC + v) / 2];
+                b[v] = a[v] * t.x - a[v + 1] * t.y;
+                b[v + 1] = a[v + 1] * t.x + a[v] * t.y;
+            }
+            F::store(y + u * VEC, b);
+        } else {
+            const int at = HALF ? u * VEC : 2 * u, other = HALF ? at + pairs : at + 1;
+            F::unpack(F::load_stream(x + at), a);
+            F::unpack(F::load_stream(x + other), b);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float2 t = cs[HALF ? at + v : u];
+                const float p = a[v];
+                a[v] = p * t.x - b[v] * t.y;
+                b[v] = b[v] * t.x + p * t.y;
+            }
+            F::store(y + at, a);
+            F::store(y + other, b);
+        }
+    }
+}
+
+template <typename T, int VEC, bool HALF>
+void launch_rotary(RotaryParams &P, cudaStream_t st) {
+    // about 1024 vectors per block, fewer rows where that leaves SMs idle
+    int64_t rows = 1024 / (int64_t(P.mats) * P.H / VEC) + 1;
+    const int64_t spread = (P.N + 2 * kSMs - 1) / (2 * kSMs);
+    const int64_t fit = kMaxRot / P.rot;
+    if (rows > spread) rows = spread;
+    if (rows > fit) rows = fit;
+    if (rows < 1) rows = 1;
+    P.rows = int(rows);
+    const size_t smem = size_t(rows) * (P.rot / 2) * sizeof(float2);
+    k_rotary<T, VEC, HALF><<<unsigned((P.N + rows - 1) / rows), 256, smem, st>>>(P);
+}
+template <typename T, int VEC>
+void launch_rotary(RotaryParams &P, bool half, cudaStream_t st) {
+    if (half) launch_rotary<T, VEC, true>(P, st);
+    else launch_rotary<T, VEC, false>(P, st);
+}
+template <typename T>
+void dispatch_rotary(RotaryParams &P, bool half, uintptr_t addresses, cudaStream_t st) {
+    // the widest vector that divides the pairs' run, the head, what is copied, and the addresses
+    const int run = half ? P.rot / 2 : P.rot;
+    auto fits = [&](int vec) {
+        return run % vec == 0 && P.D % vec == 0 && P.rot % vec == 0 && addresses % (vec * sizeof(T)) == 0;
+    };
+    if (sizeof(T) == 2 && fits(8)) launch_rotary<T, sizeof(T) == 2 ? 8 : 4>(P, half, st);
+    else if (fits(4)) launch_rotary<T, 4>(P, half, st);
+    else if (fits(2)) launch_rotary<T, 2>(P, half, st);
+    else launch_rotary<T, 1>(P, half, st);
+}
+
+// ---------------------------------------------------------------------------- norm, gate and residual
+
+// forward:  X = R + scale * drop(act(G) * (norm(B) * gamma1 + beta1)),  Z = norm(X) * gamma2 + beta2
+// norm: x / sqrt(mean(x^2) + eps), or with the mean subtracted first.
+struct NormParams {
+    const void *R, *B, *G, *X, *dX, *dZ;      // inputs (absent: null)
+    void *oX, *oZ, *dR, *dB, *dG;             // outputs (absent: null)
+    const float *gamma1, *beta1, *scale, *gamma2, *beta2;
+    float *partial;                           // [blocks][5][H] (backward)
+    int64_t N;
+    int H, layer, silu;
+    float eps, inv_h;
+    Drop drop;
+};
+
+// Sums of up to two values over the TPR threads of a row (all get them).
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float2 v, float2 *red) {
+    constexpr int W = TPR < 32 ? TPR : 32;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(kAll, v.x, o);
+        v.y += __shfl_xor_sync(kAll, v.y, o);
+    }
+    if (TPR > 32) {
+        constexpr int warps = TPR / 32;
+        const int group = threadIdx.x / TPR * warps, w = threadIdx.x / 32;
+        __syncthreads();  // the previous sums have been read
+        if ((threadIdx.x & 31) == 0) red[w] = v;
+        __syncthreads();
+        v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < warps; ++k) {
+            v.x += red[group + k].x;
+            v.y += red[group + k].y;
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+
+template <int VEC, int NV>
+__device__ __forceinline__ float vec_of(const float *p, int c, int v, float none) {
+    return p ? __ldg(p + c + v) : none;
+}
+
+template <typename T, int VEC, int NV, int TPR>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_resnorm_fwd(const NormParams P) {
+    constexpr int THREADS = TPR < 256 ? 256 : TPR;
+    constexpr int RPB = THREADS / TPR;
+    using F = Frag<T, VEC>;
+    __shared__ float2 red[THREADS / 32];
+    const int l = threadIdx.x % TPR;
+    bool ok[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) ok[k] = (l + k * TPR) * VEC < P.H;
+    for (int64_t n0 = int64_t(blockIdx.x) * RPB; n0 < P.N; n0 += int64_t(gridDim.x) * RPB) {
+        const int64_t n = n0 + threadIdx.x / TPR;
+        const bool row = n < P.N;
+        const int64_t at = n * P.H;
+        float x[NV][VEC], b[NV][VEC], g[NV][VEC];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (l + k * TPR) * VEC;
+            const bool in = row && ok[k];
+            F::unpack(in && P.R ? F::load_stream(static_cast<const T *>(P.R) + at + c) : F::zero(), x[k]);
+            F::unpack(in && P.B ? F::load_stream(static_cast<const T *>(P.B) + at + c) : F::zero(), b[k]);
+            F::unpack(in && P.G ? F::load_stream(static_cast<const T *>(P.G) + at + c) : F::zero(), g[k]);
+        }
+        if (P.B) {
+            float2 s = make_float2(0.f, 0.f);
+            if (P.layer) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) s.x += b[k][v];
+                const float mean = row_sum<TPR>(s, red).x * P.inv_h;
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) b[k][v] = ok[k] ? b[k][v] - mean : 0.f;
+            }
+            s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s.x = fmaf(b[k][v], b[k][v], s.x);
+            const float r = rsqrtf(fmaf(row_sum<TPR>(s, red).x, P.inv_h, P.eps));
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (l + k * TPR) * VEC;
+                if (!(row && ok[k])) continue;
+                const uint32_t kept = P.drop.on ? keep_bits(uint64_t(at + c), VEC, P.drop) : 0xffffffffu;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float u = fmaf(b[k][v] * r, vec_of<VEC, NV>(P.gamma1, c, v, 1.f), vec_of<VEC, NV>(P.beta1, c, v, 0.f));
+                    if (P.G) {
+                        const float sg = sigmoid(g[k][v]);
+                        u *= P.silu ? g[k][v] * sg : sg;
+                    }
+                    u = kept >> v & 1u ? u * P.drop.scale : 0.f;
+                    x[k][v] = fmaf(vec_of<VEC, NV>(P.scale, c, v, 1.f), u, x[k][v]);
+                }
+                F::store(static_cast<T *>(P.oX) + at + c, x[k]);
+            }
+        }
+        if (P.oZ) {
+            float2 s = make_float2(0.f, 0.f);
+            if (P.layer) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) s.x += x[k][v];
+                const float mean = row_sum<TPR>(s, red).x * P.inv_h;
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] - mean : 0.f;
+            }
+            s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s.x = fmaf(x[k][v], x[k][v], s.x);
+            const float r = rsqrtf(fmaf(row_sum<TPR>(s, red).x, P.inv_h, P.eps));
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (l + k * TPR) * VEC;
+                if (!(row && ok[k])) continue;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    x[k][v] = fmaf(x[k][v] * r, vec_of<VEC, NV>(P.gamma2, c, v, 1.f), vec_of<VEC, NV>(P.beta2, c, v, 0.f));
+                F::store(static_cast<T *>(P.oZ) + at + c, x[k]);
+            }
+        }
+    }
+}
+
+// backward, from the stored X and B (the norms' statistics are recomputed
+// from the row, which is in registers):
+//   n2 = norm(X): dR = dX + norm'(dZ gamma2), dgamma2 += dZ n2, dbeta2 += dZ
+//   n1 = norm(B), u = n1 gamma1 + beta1, k = keep / (1 - p):
+//   dscale += dR k act u, dG = dR scale k act' u, du = dR scale k act,
+//   dgamma1 += du n1, dbeta1 += du, dB = norm'(du gamma1)
+// with norm'(y) = r (y - n mean(y n) [- mean(y)]).  A thread keeps the column
+// sums of the rows it visits in registers; a block adds its threads' sums in
+// shared memory and writes one partial row, and k_resnorm_join adds the
+// blocks' in order.
+template <typename T, int VEC, int NV, int TPR>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_resnorm_bwd(const NormParams P) {
+    constexpr int THREADS = TPR < 256 ? 256 : TPR;
+    constexpr int RPB = THREADS / TPR;
+    using F = Frag<T, VEC>;
+    __shared__ float2 red[THREADS / 32];
+    __shared__ float cols[RPB > 1 ? THREADS * VEC * NV : 1];
+    const int l = threadIdx.x % TPR;
+    bool ok[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) ok[k] = (l + k * TPR) * VEC < P.H;
+    float sum[5][NV][VEC];  // dgamma1, dbeta1, dscale, dgamma2, dbeta2
+#pragma unroll
+    for (int a = 0; a < 5; ++a)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sum[a][k][v] = 0.f;
+    for (int64_t n0 = int64_t(blockIdx.x) * RPB; n0 < P.N; n0 += int64_t(gridDim.x) * RPB) {
+        const int64_t n = n0 + threadIdx.x / TPR;
+        const bool row = n < P.N;
+        const int64_t at = n * P.H;
+        float x[NV][VEC], b[NV][VEC], dr[NV][VEC];
+        typename F::raw rz[NV], rg[NV];
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (l + k * TPR) * VEC;
+            const bool in = row && ok[k];
+            F::unpack(in && P.X && P.dZ ? F::load_stream(static_cast<const T *>(P.X) + at + c) : F::zero(), x[k]);
+            F::unpack(in && P.B ? F::load_stream(static_cast<const T *>(P.B) + at + c) : F::zero(), b[k]);
+            F::unpack(in && P.dX ? F::load_stream(static_cast<const T *>(P.dX) + at + c) : F::zero(), dr[k]);
+            rz[k] = in && P.dZ ? F::load_stream(static_cast<const T *>(P.dZ) + at + c) : F::zero();
+            rg[k] = in && P.G ? F::load_stream(static_cast<const T *>(P.G) + at + c) : F::zero();
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s.x += x[k][v], s.y += b[k][v];
+        }
+        if (P.layer) {
+            s = row_sum<TPR>(s, red);
+            const float mx = s.x * P.inv_h, mb = s.y * P.inv_h;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] - mx : 0.f, b[k][v] = ok[k] ? b[k][v] - mb : 0.f;
+        }
+        s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s.x = fmaf(x[k][v], x[k][v], s.x), s.y = fmaf(b[k][v], b[k][v], s.y);
+        s = row_sum<TPR>(s, red);
+        const float rx = rsqrtf(fmaf(s.x, P.inv_h, P.eps)), rb = rsqrtf(fmaf(s.y, P.inv_h, P.eps));
+        if (P.dZ) {
+            float2 q = make_float2(0.f, 0.f);
+            float y[NV][VEC];
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (l + k * TPR) * VEC;
+                F::unpack(rz[k], y[k]);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float nx = x[k][v] * rx;
+                    sum[3][k][v] = fmaf(y[k][v], nx, sum[3][k][v]);
+                    sum[4][k][v] += y[k][v];
+                    if (ok[k]) y[k][v] *= vec_of<VEC, NV>(P.gamma2, c, v, 1.f);
+                    q.x = fmaf(y[k][v], nx, q.x);
+                    q.y += y[k][v];
+                }
+            }
+            q = row_sum<TPR>(q, red);
+            const float c1 = q.x * P.inv_h, c0 = P.layer ? q.y * P.inv_h : 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) dr[k][v] = fmaf(rx, y[k][v] - c0 - x[k][v] * rx * c1, dr[k][v]);
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (row && ok[k] && P.dR) F::store(static_cast<T *>(P.dR) + at + (l + k * TPR) * VEC, dr[k]);
+        if (P.B) {
+            float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (l + k * TPR) * VEC;
+                const bool in = row && ok[k];
+                const uint32_t kept = P.drop.on && in ? keep_bits(uint64_t(at + c), VEC, P.drop) : 0xffffffffu;
+                float g[VEC];
+                F::unpack(rg[k], g);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float gamma = ok[k] ? vec_of<VEC, NV>(P.gamma1, c, v, 1.f) : 0.f;
+                    const float beta = ok[k] ? vec_of<VEC, NV>(P.beta1, c, v, 0.f) : 0.f;
+                    const float sc = ok[k] ? vec_of<VEC, NV>(P.scale, c, v, 1.f) : 0.f;
+                    const float nb = b[k][v] * rb;
+                    b[k][v] = nb;
+                    const float u = fmaf(nb, gamma, beta);
+                    float act = 1.f, slope = 0.f;
+                    if (P.G) {
+                        const float sg = sigmoid(g[v]);
+                        slope = sg * (1.f - sg);
+                        act = sg;
+                        if (P.silu) slope = fmaf(g[v], slope, sg), act = g[v] * sg;
+                    }
+                    const float d = kept >> v & 1u ? dr[k][v] * P.drop.scale : 0.f;
+                    sum[2][k][v] = fmaf(d, act * u, sum[2][k][v]);
+                    const float ds = d * sc;
+                    g[v] = ds * u * slope;
+                    float du = ds * act;
+                    sum[0][k][v] = fmaf(du, nb, sum[0][k][v]);
+                    sum[1][k][v] += du;
+                    du *= gamma;
+                    dr[k][v] = du;
+                    q.x = fmaf(du, nb, q.x);
+                    q.y += du;
+                }
+                if (in && P.dG) F::store(static_cast<T *>(P.dG) + at + c, g);
+            }
+            q = row_sum<TPR>(q, red);
+            const float c1 = q.x * P.inv_h, c0 = P.layer ? q.y * P.inv_h : 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) dr[k][v] = rb * (dr[k][v] - c0 - b[k][v] * c1);
+                if (row && ok[k]) F::store(static_cast<T *>(P.dB) + at + (l + k * TPR) * VEC, dr[k]);
+            }
+        }
+    }
+    if (!P.partial) return;
+#pragma unroll
+    for (int a = 0; a < 5; ++a) {
+        float *out = P.partial + (int64_t(blockIdx.x) * 5 + a) * P.H;
+        if (RPB > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) cols[(threadIdx.x / TPR * TPR * NV + k * TPR + l) * VEC + v] = sum[a][k][v];
+            __syncthreads();
+            for (int c = threadIdx.x; c < P.H; c += THREADS) {
+                float s = 0.f;
+                for (int q = 0; q < RPB; ++q) s += cols[q * TPR * NV * VEC + c];
+                out[c] = s;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    if (ok[k]) out[(l + k * TPR) * VEC + v] = sum[a][k][v];
+        }
+    }
+}
+
+struct JoinParams {
+    const float *partial;
+    float *out[5];
+    int blocks, H;
+};
+// Column sums of the blocks' partial rows: a warp-row of 32 columns per
+// block, its 8 warps each adding every 8th row, then the 8 in order.
+__global__ void __launch_bounds__(256) k_resnorm_join(const JoinParams P) {
+    __shared__ float red[8][32];
+    float *out = P.out[blockIdx.y];
+    if (!out) return;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    float s = 0.f;
+    if (c < P.H)
+        for (int b = w; b < P.blocks; b += 8) s += P.partial[(int64_t(b) * 5 + blockIdx.y) * P.H + c];
+    red[w][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (w == 0 && c < P.H) {
+        for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
+        out[c] = s;
+    }
+}
+
+constexpr int kMaxNormWidth = 8192;
+// Blocks of the backward pass: a bound of its partial rows that depends on
+// the sizes alone.
+int64_t norm_blocks(int64_t N, int64_t H) {
+    int64_t per_sm = 8192 / H;
+    per_sm = per_sm < 2 ? 2 : (per_sm > 8 ? 8 : per_sm);
+    return N < kSMs * per_sm ? N : kSMs * per_sm;
+}
+
+template <typename T, int VEC, int NV, int TPR>
+void launch_norm(const NormParams &P, bool back, int *blocks, cudaStream_t st) {
+    constexpr int THREADS = TPR < 256 ? 256 : TPR;
+    constexpr int RPB = THREADS / TPR;
+    if (back) {
+        *blocks = int(grid_of(P.N, RPB, norm_blocks(P.N, P.H)));
+        k_resnorm_bwd<T, VEC, NV, TPR><<<*blocks, THREADS, 0, st>>>(P);
+    } else {
+        k_resnorm_fwd<T, VEC, NV, TPR><<<grid_of(P.N, RPB, kSMs * 16), THREADS, 0, st>>>(P);
+    }
+}
+// Threads per row: the power of two that covers the row's vectors, up to 1024;
+// rows beyond that take more vectors per thread.
+template <typename T, int VEC>
+void dispatch_norm(const NormParams &P, bool back, int *blocks, cudaStream_t st) {
+    const int n = (P.H + VEC - 1) / VEC;
+    if (n <= 4) launch_norm<T, VEC, 1, 4>(P, back, blocks, st);
+    else if (n <= 8) launch_norm<T, VEC, 1, 8>(P, back, blocks, st);
+    else if (n <= 16) launch_norm<T, VEC, 1, 16>(P, back, blocks, st);
+    else if (n <= 32) launch_norm<T, VEC, 1, 32>(P, back, blocks, st);
+    else if (n <= 64) launch_norm<T, VEC, 1, 64>(P, back, blocks, st);
+    else if (n <= 128) launch_norm<T, VEC, 1, 128>(P, back, blocks, st);
+    else if (n <= 256) launch_norm<T, VEC, 1, 256>(P, back, blocks, st);
+    else if (n <= 512) launch_norm<T, VEC, 1, 512>(P, back, blocks, st);
+    else if (n <= 1024) launch_norm<T, VEC, 1, 1024>(P, back, blocks, st);
+    else if constexpr (VEC == 4) launch_norm<T, VEC, 2, 1024>(P, back, blocks, st);
+    else if constexpr (VEC == 1) {
+        if (n <= 2048) launch_norm<T, VEC, 2, 1024>(P, back, blocks, st);
+        else launch_norm<T, VEC, 8, 1024>(P, back, blocks, st);
+    }
+}
+template <typename T>
+void dispatch_norm(const NormParams &P, uintptr_t addresses, bool back, int *blocks, cudaStream_t st) {
+    constexpr int WIDE = sizeof(T) == 4 ? 4 : 8;
+    auto fits = [&](int vec) { return P.H % vec == 0 && addresses % (vec * sizeof(T)) == 0; };
+    if (fits(WIDE)) dispatch_norm<T, WIDE>(P, back, blocks, st);
+    else if (sizeof(T) == 2 && fits(4)) dispatch_norm<T, 4>(P, back, blocks, st);
+    else dispatch_norm<T, 1>(P, back, blocks, st);
+}
+
+// ---------------------------------------------------------------------------- checks
+
+struct Named {
+    const void *p;
+    const char *name;
+    bool need;
+};
+// Pointers of a call without a graph: device memory of the current device.
+template <int K>
+int check_pointers(const Named (&a)[K], const char *fn) {
+    int device = -1;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess) return cuda_fail(err, fn);
+    for (const Named &x : a) {
+        if (!x.p) continue;
+        if (int rc = check_device_ptr(x.p, device, x.name)) return rc;
+    }
+    return AG_OK;
+}
+template <int K>
+int check_given(const Named (&a)[K], int align, const char *fn) {
+    for (const Named &x : a) {
+        if (x.need && !x.p) return fail(AG_ERR_INVALID_ARG, "%s: null %s", fn, x.name);
+        if (reinterpret_cast<uintptr_t>(x.p) % uintptr_t(align) != 0)
+            return fail(AG_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", fn, x.name);
+    }
+    return AG_OK;
+}
+int check_dtype(int dtype, const char *fn) {
+    return dtype == AG_F32 || dtype == AG_BF16 ? int(AG_OK) : fail(AG_ERR_DTYPE, "%s: unknown dtype %d", fn, dtype);
+}
+int check_drop(double p, const char *fn) {
+    return p >= 0.0 && p < 1.0 ? int(AG_OK) : fail(AG_ERR_INVALID_ARG, "%s: p = %g outside [0, 1)", fn, p);
+}
+int element_size(int dtype) { return dtype == AG_F32 ? 4 : 2; }
+
+int check_resnorm(const ag_resnorm *op, int64_t N, int64_t H, int dtype, const char *fn) {
+    if (!op) return fail(AG_ERR_INVALID_ARG, "%s: null parameters", fn);
+    if (N < 0 || N >= (int64_t(1) << 31) || H < 1 || H > kMaxNormWidth)
+        return fail(AG_ERR_SHAPE, "%s: N = %lld outside [0, 2^31) or H = %lld outside [1, %d]", fn, (long long)N,
+                    (long long)H, kMaxNormWidth);
+    if (int rc = check_dtype(dtype, fn)) return rc;
+    if (op->norm != AG_NORM_RMS && op->norm != AG_NORM_LAYER) return fail(AG_ERR_INVALID_ARG, "%s: unknown norm %d", fn, op->norm);
+    if (op->act != AG_ACT_SIGMOID && op->act != AG_ACT_SILU) return fail(AG_ERR_INVALID_ARG, "%s: unknown gate %d", fn, op->act);
+    if (!(op->eps >= 0.f) || !isfinite(op->eps)) return fail(AG_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+    return check_drop(op->p, fn);
+}
+
+NormParams norm_params(const ag_resnorm *op, int64_t N, int64_t H) {
+    NormParams P = {};
+    P.gamma1 = op->gamma1;
+    P.beta1 = op->beta1;
+    P.scale = op->scale;
+    P.gamma2 = op->gamma2;
+    P.beta2 = op->beta2;
+    P.N = N;
+    P.H = int(H);
+    P.layer = op->norm == AG_NORM_LAYER;
+    P.silu = op->act == AG_ACT_SILU;
+    P.eps = op->eps;
+    P.inv_h = 1.f / float(H);
+    P.drop = make_drop(op->p, op->seed, op->offset);
+    return P;
+}
+
+}  // namespace
+}  // namespace ag
+
+using namespace ag;
+
+extern "C" {
+
+int ag_dropout(const void *X, void *Y, int64_t n, double p, uint64_t seed, uint64_t offset, int dtype, void *stream) {
+    const char *fn = "ag_dropout";
+    clear_error();
+    if (n < 0 || n >= (int64_t(1) << 40)) return fail(AG_ERR_SHAPE, "%s: n = %lld outside [0, 2^40)", fn, (long long)n);
+    int rc;
+    if ((rc = check_dtype(dtype, fn)) != AG_OK) return rc;
+    if ((rc = check_drop(p, fn)) != AG_OK) return rc;
+    if (n == 0) return AG_OK;
+    const Named a[] = {{X, "X", true}, {Y, "Y", true}};
+    if ((rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
+    if ((rc = check_pointers(a, fn)) != AG_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Drop drop = make_drop(p, seed, offset);
+    if (dtype == AG_F32) launch_dropout<float, 4>(X, Y, n, drop, st);
+    else launch_dropout<bf16_t, 8>(X, Y, n, drop, st);
+    cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);
+}
+
+int ag_rotary_freqs(int64_t rot, double base, int scaling, double factor, double original, double beta_fast,
+                    double beta_slow, double *inv_freq_host, double *factor_host) {
+    const char *fn = "ag_rotary_freqs";
+    clear_error();
+    if (rot < 2 || rot > kMaxRot || rot % 2) return fail(AG_ERR_SHAPE, "%s: rot = %lld is not even in [2, %d]", fn, (long long)rot, kMaxRot);
+    if (!inv_freq_host) return fail(AG_ERR_INVALID_ARG, "%s: null inv_freq", fn);
+    if (!(base > 0.0) || !isfinite(base)) return fail(AG_ERR_INVALID_ARG, "%s: base must be positive", fn);
+    if (scaling < AG_ROPE_NONE || scaling > AG_ROPE_YARN) return fail(AG_ERR_INVALID_ARG, "%s: unknown scaling %d", fn, scaling);
+    if (scaling != AG_ROPE_NONE && (!(factor >= 1.0) || !isfinite(factor)))
+        return fail(AG_ERR_INVALID_ARG, "%s: factor must be at least 1", fn);
+    const double pi2 = 6.283185307179586;
+    if (scaling == AG_ROPE_YARN && !(original > 0.0 && isfinite(original) && beta_fast > beta_slow && beta_slow > 0.0 && base != 1.0))
+        return fail(AG_ERR_INVALID_ARG, "%s: needs original > 0, beta_fast > beta_slow > 0 and base != 1", fn);
+    if (scaling == AG_ROPE_NTK && rot > 2) base *= pow(factor, double(rot) / double(rot - 2));
+    double lo = 0.0, hi = 0.0;
+    if (scaling == AG_ROPE_YARN) {
+        // the pair that makes `turns` turns within the original range
+        auto at = [&](double turns) { return double(rot) * log(original / (turns * pi2)) / (2.0 * log(base)); };
+        lo = fmax(0.0, floor(at(beta_fast)));
+        hi = fmin(double(rot - 1), ceil(at(beta_slow)));
+    }
+    for (int64_t i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * double(i) / double(rot));
+        if (scaling == AG_ROPE_LINEAR) f /= factor;
+        if (scaling == AG_ROPE_YARN) {
+            const double r = fmin(1.0, fmax(0.0, (double(i) - lo) / fmax(hi - lo, 0.001)));
+            f = f / factor * r + f * (1.0 - r);
+        }
+        inv_freq_host[i] = f;
+    }
+    if (factor_host) *factor_host = scaling == AG_ROPE_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
+    return AG_OK;
+}
+
+int ag_rotary(const void *Q, const void *K, const int64_t *pos, const double *inv_freq, void *Qo, void *Ko, int64_t N,
+              int64_t H, int64_t heads, int64_t rot, int interleaved, float factor, int inverse, int dtype,
+              void *stream) {
+    const char *fn = "ag_rotary";
+    clear_error();
+    if (N < 0 || N >= (int64_t(1) << 31) || H < 1 || H > (int64_t(1) << 20))
+        return fail(AG_ERR_SHAPE, "%s: N = %lld outside [0, 2^31) or H = %lld outside [1, 2^20]", fn, (long long)N, (long long)H);
+    if (heads < 1 || heads > H || H % heads) return fail(AG_ERR_SHAPE, "%s: H = %lld is not heads = %lld equal heads", fn, (long long)H, (long long)heads);
+    if (rot < 2 || rot % 2 || rot > H / heads || rot > kMaxRot)
+        return fail(AG_ERR_SHAPE, "%s: rot = %lld is not even in [2, min(H / heads, %d)]", fn, (long long)rot, kMaxRot);
+    int rc;
+    if ((rc = check_dtype(dtype, fn)) != AG_OK) return rc;
+    if (!isfinite(factor)) return fail(AG_ERR_INVALID_ARG, "%s: factor must be finite", fn);
+    if (N == 0) return AG_OK;
+    const Named a[] = {{Q, "Q", true}, {Qo, "Q's output", true}, {K, "K", false}, {Ko, "K's output", K != nullptr}};
+    const Named b[] = {{pos, "pos", true}, {inv_freq, "inv_freq", true}};
+    if ((rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
+    if ((rc = check_given(b, 8, fn)) != AG_OK) return rc;
+    if ((rc = check_pointers(a, fn)) != AG_OK) return rc;
+    if ((rc = check_pointers(b, fn)) != AG_OK) return rc;
+    RotaryParams P = {};
+    P.in[0] = Q;
+    P.in[1] = K;
+    P.out[0] = Qo;
+    P.out[1] = Ko;
+    P.pos = pos;
+    P.inv_freq = inv_freq;
+    P.N = N;
+    P.mats = K ? 2 : 1;
+    P.H = int(H);
+    P.heads = int(heads);
+    P.D = int(H / heads);
+    P.rot = int(rot);
+    P.factor = factor;
+    P.sign = inverse ? -1.f : 1.f;
+    uintptr_t at = uintptr_t(Q) | uintptr_t(Qo);
+    if (K) at |= uintptr_t(K) | uintptr_t(Ko);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == AG_F32) dispatch_rotary<float>(P, !interleaved, at, st);
+    else dispatch_rotary<bf16_t>(P, !interleaved, at, st);
+    cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);
+}
+
+int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, const void *G, void *X, void *Z, int64_t N,
+                   int64_t H, int dtype, void *stream) {
+    const char *fn = "ag_resnorm_fwd";
+    clear_error();
+    int rc = check_resnorm(op, N, H, dtype, fn);
+    if (rc != AG_OK) return rc;
+    if (N == 0) return AG_OK;
+    if (!B && G) return fail(AG_ERR_INVALID_ARG, "%s: a gate without a block output", fn);
+    if (!B && X) return fail(AG_ERR_INVALID_ARG, "%s: X without a block output (the sum is R)", fn);
+    if (!B && !R) return fail(AG_ERR_INVALID_ARG, "%s: neither R nor B", fn);
+    if (!X && !Z) return fail(AG_ERR_INVALID_ARG, "%s: neither X nor Z", fn);
+    const Named a[] = {{R, "R", false}, {B, "B", false}, {G, "G", false}, {X, "X", B != nullptr}, {Z, "Z", false}};
+    const Named f[] = {{op->gamma1, "gamma1", false}, {op->beta1, "beta1", false}, {op->scale, "scale", false},
+                       {op->gamma2, "gamma2", false}, {op->beta2, "beta2", false}};
+    if ((rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
+    if ((rc = check_given(f, 4, fn)) != AG_OK) return rc;
+    if ((rc = check_pointers(a, fn)) != AG_OK) return rc;
+    if ((rc = check_pointers(f, fn)) != AG_OK) return rc;
+    NormParams P = norm_params(op, N, H);
+    P.R = R;
+    P.B = B;
+    P.G = G;
+    P.oX = X;
+    P.oZ = Z;
+    const uintptr_t at = uintptr_t(R) | uintptr_t(B) | uintptr_t(G) | uintptr_t(X) | uintptr_t(Z);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == AG_F32) dispatch_norm<float>(P, at, false, nullptr, st);
+    else dispatch_norm<bf16_t>(P, at, false, nullptr, st);
+    cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);
+}
+
+size_t ag_resnorm_scratch_bytes(int64_t N, int64_t H) {
+    if (N < 0 || N >= (int64_t(1) << 31) || H < 1 || H > kMaxNormWidth) return 0;
+    return align_up(size_t(norm_blocks(N, H)) * 5 * size_t(H) * 4);
+}
+
+int ag_resnorm_backward(const ag_resnorm *op, const void *X, const void *B, const void *G, const void *dX,
+                        const void *dZ, void *dR, void *dB, void *dG, float *dgamma1, float *dbeta1, float *dscale,
+                        float *dgamma2, float *dbeta2, int64_t N, int64_t H, int dtype, void *scratch,
+                        size_t scratch_bytes, void *stream) {
+    const char *fn = "ag_resnorm_backward";
+    clear_error();
+    int rc = check_resnorm(op, N, H, dtype, fn);
+    if (rc != AG_OK) return rc;
+    if (N > 0) {  // matrices without rows have no addresses
+        if (!B && (G || dB || dG || dgamma1 || dbeta1 || dscale))
+            return fail(AG_ERR_INVALID_ARG, "%s: a gate or a gradient of the block without its output B", fn);
+        if (!dZ && (dgamma2 || dbeta2)) return fail(AG_ERR_INVALID_ARG, "%s: dgamma2 or dbeta2 without dZ", fn);
+        if (!G && dG) return fail(AG_ERR_INVALID_ARG, "%s: dG without a gate", fn);
+        if (!dX && !dZ) return fail(AG_ERR_INVALID_ARG, "%s: neither dX nor dZ", fn);
+    }
+    float *const sums[5] = {dgamma1, dbeta1, dscale, dgamma2, dbeta2};
+    bool any = false;
+    for (float *s : sums) any = any || s;
+    const size_t need = any ? ag_resnorm_scratch_bytes(N, H) : 0;
+    if (need && (!scratch || scratch_bytes < need))
+        return fail(AG_ERR_WORKSPACE, "%s: scratch of %zu bytes, need %zu", fn, scratch_bytes, need);
+    if (reinterpret_cast<uintptr_t>(scratch) % kAlign != 0)
+        return fail(AG_ERR_WORKSPACE, "%s: scratch must be 256-byte aligned", fn);
+    const Named a[] = {{X, "X", dZ != nullptr}, {B, "B", false}, {G, "G", false}, {dX, "dX", false}, {dZ, "dZ", false},
+                       {dR, "dR", false}, {dB, "dB", B != nullptr}, {dG, "dG", false}};
+    const Named f[] = {{op->gamma1, "gamma1", false}, {op->beta1, "beta1", false}, {op->scale, "scale", false},
+                       {op->gamma2, "gamma2", false}, {op->beta2, "beta2", false}, {dgamma1, "dgamma1", false},
+                       {dbeta1, "dbeta1", false}, {dscale, "dscale", false}, {dgamma2, "dgamma2", false},
+                       {dbeta2, "dbeta2", false}, {need ? scratch : nullptr, "scratch", false}};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N > 0 && (rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
+    if ((rc = check_given(f, 4, fn)) != AG_OK) return rc;
+    if (N > 0 && (rc = check_pointers(a, fn)) != AG_OK) return rc;
+    if ((rc = check_pointers(f, fn)) != AG_OK) return rc;
+    int blocks = 0;
+    if (N > 0) {
+        NormParams P = norm_params(op, N, H);
+        P.X = X;
+        P.B = B;
+        P.G = G;
+        P.dX = dX;
+        P.dZ = dZ;
+        P.dR = dR;
+        P.dB = dB;
+        P.dG = dG;
+        P.partial = any ? static_cast<float *>(scratch) : nullptr;
+        uintptr_t at = uintptr_t(X) | uintptr_t(B) | uintptr_t(G) | uintptr_t(dX) | uintptr_t(dZ);
+        at |= uintptr_t(dR) | uintptr_t(dB) | uintptr_t(dG);
+        if (dtype == AG_F32) dispatch_norm<float>(P, at, true, &blocks, st);
+        else dispatch_norm<bf16_t>(P, at, true, &blocks, st);
+    }
+    if (any) {
+        JoinParams J;
+        J.partial = static_cast<const float *>(scratch);
+        for (int k = 0; k < 5; ++k) J.out[k] = sums[k];
+        J.blocks = blocks;
+        J.H = int(H);
+        k_resnorm_join<<<dim3(unsigned((H + 31) / 32), 5), 256, 0, st>>>(J);
+    }
+    cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);
+}
+
+}  // extern "C"

@@ -338,6 +338,189 @@ AG_API int ag_attn_backward(const ag_graph *g, const void *Q, const void *K, con
                             int dtype, void *scratch, size_t scratch_bytes, void *stream);
 
 /*
+ * Dropout from a counter-based generator (Philox4x32-10: Salmon, Moraes,
+ * Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011): element
+ * i is kept where word i % 4 of the block with counter (i / 4, offset) and
+ * key seed (both as pairs of 32-bit words, low first) is at least
+ * round(p * 2^32), as an unsigned number:
+ *   Y_i = X_i / (1 - p) where kept, else 0 (whatever X_i holds).
+ * The mask is a function of (seed, offset, i) alone and is never stored: the
+ * gradient is the same call on dY.  For features [N, H] i = n * H + h; for
+ * per-edge weights [E] (dropped edges) i is the COO ordinal.  A new mask for
+ * every step takes a new offset (or seed).
+ *
+ *   X, Y     device [n] of dtype; Y may be X
+ *   p        0 <= p < 1
+ * Errors: AG_ERR_SHAPE (n outside [0, 2^40)), AG_ERR_DTYPE,
+ * AG_ERR_INVALID_ARG (null or misaligned pointer, p outside [0, 1)),
+ * AG_ERR_DEVICE (not memory of the current device), AG_ERR_CUDA.
+ */
+AG_API int ag_dropout(const void *X, void *Y, int64_t n, double p, uint64_t seed, uint64_t offset, int dtype,
+                      void *stream);
+
+/*
+ * Rotary positions of the rows of one or two feature matrices (queries and
+ * keys ahead of an attention): a node's position enters every score only
+ * through differences pos[dst] - pos[src].  A row is `heads` heads of
+ * D = H / heads columns; pair i < rot / 2 of a head is columns (i, i + rot / 2)
+ * (interleaved = 0) or (2 i, 2 i + 1) (interleaved = 1), and columns from rot
+ * on are copied.  With a = pos[n] * inv_freq[i] (fp64, reduced in turns):
+ *   y0 = factor * (x0 cos a - x1 sin a),  y1 = factor * (x1 cos a + x0 sin a)
+ * inverse = 1 rotates by -a: with the same factor that is the gradient.
+ *
+ *   Q, K       device [N, H] of dtype; K may be NULL (then Ko is ignored)
+ *   pos        device int64 [N], any sign
+ *   inv_freq   device double [rot / 2]
+ *   Qo, Ko     device [N, H] of dtype; each may be its input
+ *   heads      1 <= heads, H % heads == 0; for ag_diff_attn_* pass 2 * heads
+ *              there, one for every map
+ *   rot        even, 2 <= rot <= min(D, 4096)
+ * Errors: AG_ERR_SHAPE, AG_ERR_DTYPE, AG_ERR_INVALID_ARG (null or misaligned
+ * pointer, factor not finite), AG_ERR_DEVICE, AG_ERR_CUDA.
+ */
+AG_API int ag_rotary(const void *Q, const void *K, const int64_t *pos, const double *inv_freq, void *Qo, void *Ko,
+                     int64_t N, int64_t H, int64_t heads, int64_t rot, int interleaved, float factor, int inverse,
+                     int dtype, void *stream);
+
+/*
+ * Frequencies for ag_rotary (host arithmetic, no CUDA call):
+ * inv_freq[i] = base^(-2 i / rot), and ways to stretch them by `factor` beyond
+ * the `original` range of positions:
+ *   AG_ROPE_LINEAR  inv_freq / factor (positions interpolated)
+ *   AG_ROPE_NTK     base * factor^(rot / (rot - 2)) in place of base
+ *   AG_ROPE_YARN    inv_freq / factor for pairs that make fewer than beta_slow
+ *                   turns within `original` positions, unchanged for more than
+ *                   beta_fast, a linear ramp over the pairs between; and
+ *                   *factor_host = 0.1 ln(factor) + 1 for ag_rotary's factor
+ *                   (1 for the others)
+ *   inv_freq_host   host double [rot / 2], written
+ *   factor_host     host double, written (may be NULL)
+ * Errors: AG_ERR_SHAPE (rot not even in [2, 4096]), AG_ERR_INVALID_ARG (null
+ * inv_freq_host, base <= 0, unknown scaling, factor < 1, yarn without
+ * original > 0 and beta_fast > beta_slow > 0).
+ */
+typedef enum ag_rope_scaling { AG_ROPE_NONE = 0, AG_ROPE_LINEAR = 1, AG_ROPE_NTK = 2, AG_ROPE_YARN = 3 } ag_rope_scaling;
+AG_API int ag_rotary_freqs(int64_t rot, double base, int scaling, double factor, double original, double beta_fast,
+                           double beta_slow, double *inv_freq_host, double *factor_host);
+
+/*
+ * Differential edge-softmax attention: every head has two softmax maps over a
+ * destination row's edges (as in ag_attn_fwd), and the second one, times the
+ * head's learned factor lambda, is subtracted from the first.  With
+ * d = H / (2 heads), columns [2 d j, 2 d (j + 1)) of a row belong to head j:
+ * of Q and K the first d to map 1 and the next d to map 2, of V and Y all 2 d:
+ *   s_m,e     = scale * dot(Q_m[dst_e], K_m[src_e])            m = 1, 2
+ *   alpha_m   = softmax of s_m over the edges into each row
+ *   Y[r]      = sum over edges e into r of u_e (alpha_1,e - lambda alpha_2,e) V[src_e]
+ *   lse_m[r]  = log of the sum over r's edges of exp(s_m)
+ * u_e = 1, or with dropout (p > 0) keep / (1 - p): the mask of ag_dropout over
+ * a COO-ordered [E, heads] array, one truth value for both maps.  Rows without
+ * edges give Y = 0 and lse = -inf.  Scores, statistics and sums are fp32.
+ *
+ *   Q, K, V  device [N, H] of dtype
+ *   lam      device float [heads]
+ *   scale    finite factor of the scores (1/sqrt(d) for scaled dot products)
+ *   p        0 <= p < 1, with seed and offset as in ag_dropout
+ *   Y        device [N, H] of dtype, fully written
+ *   lse      device float [N, heads, 2], fully written (for the backward pass)
+ *   heads    1 <= heads <= 256, H = 2 heads d, 1 <= d <= 256
+ *   scratch  device buffer, 256-byte aligned, of
+ *            ag_diff_attn_scratch_bytes(g, H, heads) bytes (never O(E heads));
+ *            its contents are scratch only: calls that may overlap take one each
+ * Errors as ag_attn_fwd; AG_ERR_SHAPE for heads that do not fit H,
+ * AG_ERR_INVALID_ARG also for p outside [0, 1) and misaligned pointers.
+ */
+AG_API size_t ag_diff_attn_scratch_bytes(const ag_graph *g, int64_t H, int64_t heads);
+AG_API int ag_diff_attn_fwd(const ag_graph *g, const void *Q, const void *K, const void *V, const float *lam,
+                            float scale, double p, uint64_t seed, uint64_t offset, void *Y, float *lse, int64_t H,
+                            int64_t heads, int dtype, void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * Gradients of ag_diff_attn_fwd for the upstream gradient dY.  With
+ * da_e = u_e dot(dY[dst_e], V[src_e]) and D_m[r] = sum over r's edges of
+ * alpha_m,e da_e:
+ *   ds_1,e  = scale alpha_1,e (da_e - D_1[dst_e])
+ *   ds_2,e  = -lambda scale alpha_2,e (da_e - D_2[dst_e])
+ *   dQ_m[r] = sum over edges e into r of ds_m,e K_m[src_e]
+ *   dK_m[s] = sum over edges e out of s of ds_m,e Q_m[dst_e]
+ *   dV[s]   = sum over edges e out of s of u_e (alpha_1,e - lambda alpha_2,e) dY[dst_e]
+ *   dlam    = -sum over rows r of D_2[r]
+ * The maps and the dropout mask are recomputed, from lse and from (p, seed,
+ * offset): pass what the forward call took and wrote.
+ *
+ *   dQ, dK, dV  device [N, H] of dtype, fully written
+ *   dlam        device float [heads], fully written
+ *   other arguments and errors as ag_diff_attn_fwd (same scratch size)
+ */
+AG_API int ag_diff_attn_backward(const ag_graph *g, const void *Q, const void *K, const void *V, const float *lam,
+                                 float scale, double p, uint64_t seed, uint64_t offset, const float *lse,
+                                 const void *dY, void *dQ, void *dK, void *dV, float *dlam, int64_t H, int64_t heads,
+                                 int dtype, void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * What lies between one block of a network and the next: a norm of the block's
+ * output, its gate, dropout and residual scale, the residual sum, and the norm
+ * ahead of the next block, in one pass over the rows:
+ *   X = R + scale * drop(act(G) * (norm(B) * gamma1 + beta1))
+ *   Z = norm(X) * gamma2 + beta2
+ * norm(x) = x / sqrt(mean(x^2) + eps) (AG_NORM_RMS), or the same of
+ * x - mean(x) (AG_NORM_LAYER); act is the logistic function or x times it
+ * (AG_ACT_SILU); drop is ag_dropout over [N, H].  Z is the norm of the fp32
+ * sum, before it is rounded to X.  Every part may be left out (NULL): gamma
+ * and scale are then 1, beta 0; without G no gate, without R the sum starts at
+ * 0, without Z no second norm.  Without B (then no G and no X) Z is the norm
+ * of R alone.  A norm of every head is the same call on [N * heads, D].
+ */
+typedef enum ag_norm { AG_NORM_RMS = 0, AG_NORM_LAYER = 1 } ag_norm;
+typedef enum ag_act { AG_ACT_SIGMOID = 0, AG_ACT_SILU = 1 } ag_act;
+typedef struct ag_resnorm {
+    const float *gamma1, *beta1; /* device [H] or NULL: the block's norm */
+    const float *scale;          /* device [H] or NULL: the residual scale */
+    const float *gamma2, *beta2; /* device [H] or NULL: the next norm */
+    double p;                    /* dropout, 0 <= p < 1, as in ag_dropout */
+    uint64_t seed, offset;
+    float eps;                   /* >= 0 */
+    int32_t norm, act;           /* ag_norm, ag_act */
+} ag_resnorm;
+
+/*
+ *   R, B, G  device [N, H] of dtype
+ *   X, Z     device [N, H] of dtype, fully written; X may be R, Z may be B
+ *   N, H     0 <= N < 2^31, 1 <= H <= 8192
+ * Errors: AG_ERR_SHAPE, AG_ERR_DTYPE, AG_ERR_INVALID_ARG (null op, X missing
+ * with B, parts that do not go together, unknown norm or act, eps or p outside
+ * their range, misaligned pointer), AG_ERR_DEVICE, AG_ERR_CUDA.
+ */
+AG_API int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, const void *G, void *X, void *Z,
+                          int64_t N, int64_t H, int dtype, void *stream);
+
+/*
+ * Gradients of ag_resnorm_fwd for the gradients dX and dZ of its outputs
+ * (either may be NULL: zero).  X is the stored sum (R where there was no B);
+ * the norms' statistics and the dropout mask are recomputed.  With n = norm(X),
+ * r its reciprocal deviation, y = dZ gamma2 (and the same for B):
+ *   dR = dX + r (y - n mean(y n) [- mean(y), AG_NORM_LAYER])
+ *   dG, dB, and the column sums dgamma1, dbeta1, dscale, dgamma2, dbeta2 over
+ *   the rows by the chain rule from dR
+ * dR is the gradient of R and of X alike.  Outputs that are NULL are left out
+ * (dB is written whenever B is given).
+ *
+ *   X        device [N, H] of dtype (needed with dZ)
+ *   B, G     as in the forward call
+ *   dR, dB, dG  device [N, H] of dtype; dR may be dX, dB may be B
+ *   dgamma1, dbeta1, dscale, dgamma2, dbeta2  device float [H], fully written
+ *   scratch  device buffer, 256-byte aligned, of ag_resnorm_scratch_bytes(N, H)
+ *            bytes; not needed without a column sum
+ * The column sums are added in an order fixed by N and H (no atomics).
+ * Errors as ag_resnorm_fwd, and AG_ERR_WORKSPACE.
+ */
+AG_API size_t ag_resnorm_scratch_bytes(int64_t N, int64_t H);
+AG_API int ag_resnorm_backward(const ag_resnorm *op, const void *X, const void *B, const void *G, const void *dX,
+                               const void *dZ, void *dR, void *dB, void *dG, float *dgamma1, float *dbeta1,
+                               float *dscale, float *dgamma2, float *dbeta2, int64_t N, int64_t H, int dtype,
+                               void *scratch, size_t scratch_bytes, void *stream);
+
+/*
  * One whole aggregation step from HOST buffers: copies w, X and dY to the
  * device staging area, runs the forward pass and the fused backward pass
  * (ag_backward), and copies Y, dX and dw back.  The copy of dY and the copies

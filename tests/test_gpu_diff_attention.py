@@ -1,0 +1,259 @@
+"""Differential edge-softmax attention (CUDA path through the C ABI) against
+the 64-bit oracle; the bounds are derived in layer_oracle.diff_bounds."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from tests import layer_oracle as lo
+from tests.gpu_helpers import assert_within, bits, host, lib
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def agb():
+    return lib()
+
+
+def _tensors(N, heads, d, dtype, seed, shift=0):
+    H = 2 * heads * d
+    out = []
+    for k in range(4):
+        t = workloads.features(N, H, dtype, seed * 1000 + k, DEV)
+        if shift:  # the same values `shift` elements into a larger buffer
+            big = torch.zeros(t.numel() + shift, dtype=dtype, device=DEV)
+            big[shift:].copy_(t.view(-1))
+            t = big[shift:].view(N, H)
+        out.append(t)
+    lam = (0.2 + 0.6 * torch.rand(heads, generator=torch.Generator().manual_seed(seed))).to(DEV)
+    return (*out, lam)
+
+
+def _check(agb, src, dst, N, heads, d, dtype, p=0.0, seed=3, shift=0, what=""):
+    s32, d32 = (torch.as_tensor(np.asarray(x, np.int32)).to(DEV) for x in (src, dst))
+    g = agb.ag_graph_lower(s32, d32, N)
+    Q, K, V, G, lam = _tensors(N, heads, d, dtype, seed, shift)
+    scale = d ** -0.5
+    drop = dict(p=p, seed=(1 << 63) + seed, offset=(1 << 33) + 5)
+    Y, lse = agb.ag_diff_attn_fwd(g, Q, K, V, lam, scale, **drop)
+    grads = agb.ag_diff_attn_backward(g, Q, K, V, lam, scale, lse, G, **drop)
+    torch.cuda.synchronize()
+    src, dst = np.asarray(src, np.int64), np.asarray(dst, np.int64)
+    E = len(src)
+    h64 = [host(t).astype(np.float64) for t in (Q, K, V, G)]
+    u = lo.drop_factors(E * heads, p, drop["seed"], drop["offset"]).reshape(E, heads)
+    # the scale is an fp32 argument
+    args = (src, dst, N, *h64[:3], host(lam).astype(np.float64), float(np.float32(scale)))
+    ref = lo.diff_attention(*args, u, h64[3])
+    bound = lo.diff_bounds(*args, u, ref, dtype, h64[3])
+    assert_within(Y, ref["Y"], bound["Y"], 1.0, f"{what} Y")
+    fin = np.isfinite(ref["lse"])
+    got = host(lse)
+    assert np.array_equal(np.isfinite(got), fin) and np.all(got[~fin] == -np.inf)
+    assert_within(torch.as_tensor(got[fin]), ref["lse"][fin], bound["lse"][fin], 1.0, f"{what} lse")
+    for t, name in zip(grads, ("dQ", "dK", "dV", "dlam")):
+        assert_within(t, ref[name], bound[name], 1.0, f"{what} {name}")
+    # a second run gives the same bits
+    Y2, lse2 = agb.ag_diff_attn_fwd(g, Q, K, V, lam, scale, **drop)
+    again = agb.ag_diff_attn_backward(g, Q, K, V, lam, scale, lse2, G, **drop)
+    torch.cuda.synchronize()
+    for a, b in zip((Y, lse) + grads, (Y2, lse2) + again):
+        assert torch.equal(bits(a), bits(b))
+    return g
+
+
+def _random(seed, N=300, E=2500, hub=0):
+    rng = np.random.default_rng(seed)
+    src = np.concatenate([rng.integers(0, N, E), rng.integers(0, N, hub)])
+    dst = np.concatenate([rng.integers(0, 2 * N // 3, E), np.full(hub, 5)])
+    return src, dst, N
+
+
+# every lane count per map, with and without a whole vector, more than one
+# vector per lane, one head to many, sizes that fill no power of two
+SIZES = [(1, 1), (3, 1), (1, 2), (1, 3), (2, 4), (5, 4), (20, 4), (40, 2), (1, 8), (16, 8), (33, 8), (3, 12), (4, 16), (7, 16),
+         (2, 20), (5, 24), (1, 32), (6, 32), (2, 33), (2, 64), (1, 100), (1, 127), (2, 128), (1, 200), (1, 256)]
+
+
+@pytest.mark.parametrize("heads,d", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_head_sizes(agb, heads, d, dtype):
+    src, dst, N = _random(heads * 1000 + d, hub=400)
+    _check(agb, src, dst, N, heads, d, dtype, p=0.25 if (heads + d) % 2 else 0.0, what=f"{heads}x{d}")
+
+
+@pytest.mark.parametrize("heads,d,dtype,shift", [(4, 16, torch.float32, 1), (4, 16, torch.bfloat16, 1),
+                                                 (2, 64, torch.bfloat16, 4), (1, 8, torch.bfloat16, 2),
+                                                 (1, 128, torch.float32, 2)])
+def test_addresses_without_a_wide_vector(agb, heads, d, dtype, shift):
+    src, dst, N = _random(17)
+    _check(agb, src, dst, N, heads, d, dtype, p=0.1, shift=shift, what=f"shift {shift}")
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.9])
+@pytest.mark.parametrize("heads", [1, 2, 3, 4, 6])
+def test_dropout_of_the_maps(agb, heads, p):
+    src, dst, N = _random(heads)
+    _check(agb, src, dst, N, heads, 8, torch.float32, p=p, what=f"p {p}")
+
+
+@pytest.mark.parametrize("heads,d,dtype", [(2, 8, torch.float32), (4, 16, torch.bfloat16), (1, 6, torch.float32)])
+def test_rows_cut_by_many_tiles(agb, heads, d, dtype):
+    # destinations of 40,000 and 700 edges, a source of 9,000, empty rows, duplicates
+    rng = np.random.default_rng(21)
+    N = 5000
+    src = np.concatenate([rng.integers(0, N, 31000), np.full(9000, 8), rng.integers(0, N, 3700), [7, 7, 7]])
+    dst = np.concatenate([np.full(31000, 17), np.where(np.arange(9000) % 2, 17, rng.integers(0, N, 9000)),
+                          rng.integers(0, 200, 3000), np.full(700, 31), [9, 9, 9]])
+    g = _check(agb, src, dst, N, heads, d, dtype, p=0.1, what="skewed")
+    assert g.stats["long_spanning_rows_f"] >= 1 and g.stats["long_spanning_rows_t"] >= 1
+    assert g.stats["spanning_rows_f"] > g.stats["long_spanning_rows_f"]
+
+
+@pytest.mark.parametrize("name,dtype,heads,p", [("uniform", torch.float32, 1, 0.0), ("sbm", torch.float32, 2, 0.1),
+                                                ("rmat16", torch.bfloat16, 4, 0.1), ("twohop", torch.float32, 4, 0.0)])
+def test_configurations(agb, name, dtype, heads, p):
+    wl = workloads.make(name, seed=4, device=DEV)
+    _check(agb, host(wl.src), host(wl.dst), wl.N, heads, wl.H // (2 * heads), dtype, p=p, what=name)
+
+
+def test_one_edge_rows_self_loops_and_one_node(agb):
+    N = 200
+    rng = np.random.default_rng(2)
+    _check(agb, rng.integers(0, N, N), np.arange(N), N, 2, 8, torch.float32, what="one edge each")
+    _check(agb, np.zeros(5, int), np.zeros(5, int), 1, 2, 4, torch.float32, p=0.4, what="one node")
+    _check(agb, np.array([3]), np.array([3]), 33, 1, 4, torch.bfloat16, what="one edge")
+
+
+def test_a_graph_without_edges(agb):
+    z = torch.zeros(0, dtype=torch.int32, device=DEV)
+    g = agb.ag_graph_lower(z, z, 70)
+    Q, K, V, G, lam = _tensors(70, 3, 4, torch.float32, 1)
+    Y, lse = agb.ag_diff_attn_fwd(g, Q, K, V, lam, 0.5)
+    out = agb.ag_diff_attn_backward(g, Q, K, V, lam, 0.5, lse, G)
+    torch.cuda.synchronize()
+    assert not Y.any() and torch.all(lse == -float("inf")) and not any(t.any() for t in out)
+
+
+def test_large_scores_and_equal_scores(agb):
+    # scores of several hundred (exp of the raw score overflows fp32), and rows of equal scores
+    src, dst, N = _random(4)
+    g = agb.ag_graph_lower(*(torch.as_tensor(x.astype(np.int32)).to(DEV) for x in (src, dst)), N)
+    Q, K, V, G, lam = _tensors(N, 2, 8, torch.float32, 6)
+    for q, scale in ((Q * 64, 8.0), (torch.zeros_like(Q), 1.0)):
+        Y, lse = agb.ag_diff_attn_fwd(g, q, K, V, lam, scale)
+        torch.cuda.synchronize()
+        args = (src, dst, N, *(host(t).astype(np.float64) for t in (q, K, V)), host(lam).astype(np.float64), scale)
+        ref = lo.diff_attention(*args)
+        bound = lo.diff_bounds(*args, np.ones((len(src), 2)), ref, torch.float32)
+        assert_within(Y, ref["Y"], bound["Y"], 1.0, "Y")
+
+
+def test_infinities_and_nan_stay_in_their_rows_and_out_of_dropped_edges(agb):
+    # edges 0 -> 5, 1 -> 5, 2 -> 6; K[1] infinite against a positive query, then V[1] NaN
+    src, dst, N = np.array([0, 1, 2]), np.array([5, 5, 6]), 8
+    g = agb.ag_graph_lower(*(torch.as_tensor(x.astype(np.int32)).to(DEV) for x in (src, dst)), N)
+    Q, K, V, _, lam = _tensors(N, 1, 4, torch.float32, 8)
+    clean, _ = agb.ag_diff_attn_fwd(g, Q, K, V, lam, 0.5)
+    Kbad = K.clone()
+    Kbad[1, 0] = float("inf")
+    Y, _ = agb.ag_diff_attn_fwd(g, Q, Kbad, V, lam, 0.5)
+    rest = [r for r in range(N) if r != 5]
+    assert torch.equal(Y[rest], clean[rest])
+    want_nan = bool(Q[5, 0] > 0)  # exp(inf - inf)
+    assert bool(torch.isnan(Y[5]).all()) == want_nan
+    # a dropped edge's V is not read into the sum
+    seed = next(s for s in range(100) if lo.keep_mask(3, 0.5, s, 0).tolist() == [True, False, True])
+    Vbad = V.clone()
+    Vbad[1] = float("nan")
+    Y, lse = agb.ag_diff_attn_fwd(g, Q, K, Vbad, lam, 0.5, p=0.5, seed=seed)
+    Yok, lse2 = agb.ag_diff_attn_fwd(g, Q, K, V, lam, 0.5, p=0.5, seed=seed)
+    torch.cuda.synchronize()
+    if not torch.isnan(Y).any():
+        assert torch.equal(Y, Yok)
+    assert torch.equal(lse, lse2) and torch.equal(Y[6], Yok[6])
+
+
+def test_capture_replay_and_two_streams(agb):
+    src, dst, N = _random(9, hub=3000)
+    g = agb.ag_graph_lower(*(torch.as_tensor(x.astype(np.int32)).to(DEV) for x in (src, dst)), N)
+    args = [_tensors(N, 2, 16, torch.bfloat16, s) for s in (1, 2)]
+
+    def step(t, stream=None):
+        Q, K, V, G, lam = t
+        Y, lse = agb.ag_diff_attn_fwd(g, Q, K, V, lam, 0.25, p=0.1, seed=7, stream=stream)
+        return (Y, lse) + agb.ag_diff_attn_backward(g, Q, K, V, lam, 0.25, lse, G, p=0.1, seed=7, stream=stream)
+    want = [step(t) for t in args]
+    torch.cuda.synchronize()
+    # two streams at once on one graph: every call has scratch of its own
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(step(args[i], s if i == 0 else s.cuda_stream))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(bits(a), bits(b)) for a, b in zip(out, want[i]))
+    # two captured graphs, replayed on two streams at once
+    graphs, outs = [], []
+    for t in args:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            outs.append(step(t))
+        graphs.append(cg)
+    for o in outs:
+        for t in o:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for cg, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                cg.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip(outs[i], want[i]))
+
+
+def test_refusals(agb):
+    wl = workloads.make("uniform", seed=1, device=DEV)
+    g = agb.ag_graph_lower(wl.src, wl.dst, wl.N)
+    X, lam = wl.X, torch.ones(2, device=DEV)
+    Y, lse = agb.ag_diff_attn_fwd(g, X, X, X, lam, 1.0)
+    bad = [lambda: agb.ag_diff_attn_fwd(g, X, X, X, lam, float("inf")),
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, lam, 1.0, p=1.0),
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, lam, 1.0, seed=-1),
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, torch.ones(3, device=DEV), 1.0),     # 16 is not 6 d
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, torch.ones(0, device=DEV), 1.0),
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, lam.double(), 1.0),
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, lam.cpu(), 1.0),
+           lambda: agb.ag_diff_attn_fwd(g, X, X.bfloat16(), X, lam, 1.0),
+           lambda: agb.ag_diff_attn_fwd(g, X, X[:-1], X, lam, 1.0),
+           lambda: agb.ag_diff_attn_fwd(g, X.t().contiguous().t(), X, X, lam, 1.0),
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, lam, 1.0, Y=Y.bfloat16()),
+           lambda: agb.ag_diff_attn_fwd(g, X, X, X, lam, 1.0, lse=lse[:-1]),
+           lambda: agb.ag_diff_attn_backward(g, X, X, X, lam, 1.0, lse.double(), X),
+           lambda: agb.ag_diff_attn_backward(g, X, X, X, lam, 1.0, lse[:, :1], X),
+           lambda: agb.ag_diff_attn_backward(g, X, X, X, lam, 1.0, lse, X, p=-0.1)]
+    for call in bad:
+        with pytest.raises(agb.AggraphError):
+            call()
+    # the C entry: scratch too small, misaligned, missing; host memory; a head that is too wide
+    P = lambda t: ctypes.c_void_p(t.data_ptr())
+    n = int(agb.lib.ag_diff_attn_scratch_bytes(g.handle, 16, 2))
+    scr = torch.empty(n + 256, dtype=torch.uint8, device=DEV)
+
+    def call(q=P(X), s=P(scr), size=n, H=16, heads=2, dtype=0):
+        return agb.lib.ag_diff_attn_fwd(g.handle, q, P(X), P(X), P(lam), 1.0, 0.0, 0, 0, P(Y), P(lse), H, heads, dtype, s,
+                                        size, None)
+    assert call() == 0
+    assert call(s=None) == 7 and call(size=n - 1) == 7 and call(s=ctypes.c_void_p(scr.data_ptr() + 8)) == 7
+    assert call(q=None) == 1 and call(q=ctypes.c_void_p(X.data_ptr() + 2)) == 1
+    assert call(q=P(torch.zeros(wl.N, 16))) == 4
+    assert call(H=17) == 2 and call(H=2 * 257, heads=1) == 2 and call(H=16, heads=0) == 2 and call(dtype=9) == 3
+    assert agb.lib.ag_diff_attn_scratch_bytes(g.handle, 17, 2) == 0
+    torch.cuda.synchronize()
