@@ -30,17 +30,18 @@
 //   kDKV             source rows of the transpose CSR; D known.
 // No per-edge array is written or read besides the CSR itself.
 //
-// A warp walks one tile of T consecutive CSR positions (the tile schedule of
-// the other aggregations).  2 DL lanes hold one head of one gathered row (DL
-// lanes per map, NV vectors of VEC features per lane), head slots fill the
-// warp up, and the remaining factor splits a row's edges over lane groups
-// ("subs") that are summed at the row's end.  A lane's columns of K belong to
-// its own map; its columns of V take the weights of both maps, the other
-// one's by a shuffle.  Rows cut by tile boundaries leave fp32 partials that a
-// fix-up kernel adds in tile order, so results are bitwise reproducible.
+// 2 DL lanes hold one head of one gathered row (DL lanes per map, NV vectors
+// of VEC features per lane), and as many heads as fit share a lane group of a
+// warp; each group walks a tile of T consecutive CSR positions of its own (the
+// tile schedule of the other aggregations), the wide heads of one row in
+// several groups.  A lane's columns of K belong to its own map; its columns of
+// V take the weights of both maps, the other one's by a shuffle.  Rows cut by
+// tile boundaries leave fp32 partials that a fix-up kernel adds in tile order,
+// so results are bitwise reproducible.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "aggraph.h"
 #include "frag.cuh"
@@ -51,7 +52,8 @@ namespace ag {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 4;            // warps (tiles) per block
+constexpr int kWarps = 2;            // warps per block
+constexpr int kMinBlocks = 8;        // per SM: at most 128 registers a thread
 constexpr int kZeroPerWarp = 32;     // rows without edges per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -71,8 +73,9 @@ struct DiffParams {
     void *out_a, *out_b;         // Y | dQ | dK, dV
     float *partial;              // [2 * n_tiles] slots of `slot` floats
     int64_t slot;
-    int64_t n_nz, n_zero, n_tiles;
+    int64_t n_zero, n_tiles;
     int64_t E;
+    int n_nz;
     unsigned tile_blocks;
     int T, H, heads, d, hb_log2;
     float c2;                    // scale * log2(e)
@@ -94,20 +97,41 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// Edges of a row in flight per sub.
-constexpr int edges_in_flight(int nv) { return nv == 1 ? 4 : (nv == 2 ? 2 : 1); }
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-template <typename T, int VEC, int DL, int NV, int MODE>
-__global__ void __launch_bounds__(kWarps * 32) k_diff_walk(const DiffParams P) {
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16) {
+        cp_async16(dst, src);
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+    }
+}
+
+// A running maximum is replaced only by a score beyond it by this much (in
+// powers of two): sums of exp2(x - m) stay below 2^(40 + 31).
+constexpr float kSlack = 40.f;
+
+// Positions that a lane group takes at a time while no row ends among them.
+// Two such units are in flight: 8 KB of shared memory a warp.
+constexpr int unit_positions(int nv) { return nv == 1 ? 4 : (nv == 2 ? 2 : 1); }
+
+template <typename T, int VEC, int DL, int NV, int MODE, bool DROP>
+__global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_walk(const DiffParams P) {
     using F = Frag<T, VEC>;
     using raw = typename F::raw;
-    constexpr int U = edges_in_flight(NV);
+    constexpr int PIECE = F::kBytes;
+    constexpr bool RING = PIECE >= 4;            // cp.async moves 4 bytes at least: else loads where they are used
+    constexpr int U = unit_positions(NV);
     constexpr int HL = 2 * DL;
+    constexpr int kRowBytes = NV * 32 * PIECE;   // a warp's pieces of one gathered row each
+    constexpr int kPosBytes = 2 * kRowBytes;
+    constexpr int kRing = RING ? 2 * U * kPosBytes : 16;
+    constexpr int kStatRing = RING && MODE == kDKV ? 2 * U * 32 * 8 : 0;
+    __shared__ __align__(16) unsigned char ring_mem[kWarps][kRing + kStatRing];
     const int lane = threadIdx.x & 31;
     const int head_slots = 1 << P.hb_log2;
-    const int sub_lanes = HL << P.hb_log2;       // lanes of one sub
-    const int nsub = 32 / sub_lanes;
-    const int sub = lane / sub_lanes;
+    const int group_lanes = HL << P.hb_log2;     // lanes that walk one tile
     const int hs = (lane / HL) & (head_slots - 1);
     const int map = (lane / DL) & 1;
     const int l = lane & (DL - 1);
@@ -120,30 +144,27 @@ __global__ void __launch_bounds__(kWarps * 32) k_diff_walk(const DiffParams P) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) ok[k] = live && (l + k * DL) * VEC < P.d;
 
-    auto load_row = [&](const void *base, int64_t row, bool valid, raw (&r)[NV]) {
+    auto load_row = [&](const void *base, int64_t row, raw (&r)[NV]) {
         const T *p = static_cast<const T *>(base) + row * P.H + col0;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) r[k] = valid && ok[k] ? F::load(p + k * DL * VEC) : F::zero();
+        for (int k = 0; k < NV; ++k) r[k] = ok[k] ? F::load(p + k * DL * VEC) : F::zero();
     };
-    auto store_row = [&](void *base, int64_t row, const float (&v)[NV][VEC]) {
-        T *p = static_cast<T *>(base) + row * P.H + col0;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (ok[k]) F::store(p + k * DL * VEC, v[k]);
-    };
-    const int64_t stat_col = int64_t(live ? head : 0) * 2 + map;   // of [N, heads, 2]
+    const int stat_col = (live ? head : 0) * 2 + map;   // of [N, heads, 2]
 
     if (blockIdx.x >= P.tile_blocks) {  // rows without edges
         const int64_t z0 = (int64_t(blockIdx.x - P.tile_blocks) * kWarps + (threadIdx.x >> 5)) * kZeroPerWarp;
-        float z[NV][VEC];
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) z[k][v] = 0.f;
-        for (int i = sub; i < kZeroPerWarp && z0 + i < P.n_zero; i += nsub) {
+        for (int i = lane / group_lanes; i < kZeroPerWarp && z0 + i < P.n_zero; i += 32 / group_lanes) {
             const int64_t row = P.zero_rows[z0 + i];
-            store_row(P.out_a, row, z);
-            if (MODE == kDKV) store_row(P.out_b, row, z);
+            float z[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) z[v] = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (ok[k]) {
+                    const int64_t at = row * P.H + col0 + k * DL * VEC;
+                    F::store(static_cast<T *>(P.out_a) + at, z);
+                    if (MODE == kDKV) F::store(static_cast<T *>(P.out_b) + at, z);
+                }
             if (live && l == 0) {
                 if (MODE == kFwd) P.lse_out[row * P.heads * 2 + stat_col] = -INFINITY;
                 if (MODE == kDQ) P.stat[row * P.heads * 2 + stat_col] = make_float2(0.f, 0.f);
@@ -151,286 +172,375 @@ __global__ void __launch_bounds__(kWarps * 32) k_diff_walk(const DiffParams P) {
         }
         return;
     }
-    const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (t >= P.n_tiles) return;  // whole warps
-    const int64_t p0 = t * P.T;
-    const int len = int(P.E - p0 < P.T ? P.E - p0 : P.T);
-    const int32_t *col = P.col + p0;
+    // a tile per lane group; groups behind the last tile walk none (len 0)
+    // (the last tiles first: nodes of few edges, whose tiles hold many rows and
+    // take longest, tend to have the high ids)
+    const int64_t t0 = (int64_t(P.tile_blocks - 1 - blockIdx.x) * kWarps + (threadIdx.x >> 5)) * (32 / group_lanes);
+    if (t0 >= P.n_tiles) return;  // whole warps
+    const int64_t t = t0 + lane / group_lanes;
+    const bool tile = t < P.n_tiles;
+    const int64_t p0 = tile ? t * P.T : 0;
+    const int len = tile ? int(P.E - p0 < P.T ? P.E - p0 : P.T) : 0;
+    const int steps = int(P.E - t0 * P.T < P.T ? P.E - t0 * P.T : P.T);  // the first group's: the longest
 
     const float lam = live ? P.lam[head] : 0.f;
     const float sign = map ? -lam : 1.f;
 
-    // the open row, and the next one's id, end and owner rows ahead of use
-    int64_t r = P.tile_nz[t];
-    bool before = P.nz_rowptr[r] < p0;
-    int row = 0, row_end = 0;
-    int next_row = P.nz_rows[r];
-    int next_end = int(P.nz_rowptr[r + 1] - p0);
+    // the open row, the next one with its owner rows, and the id and end of the one after
+    int r = tile ? P.tile_nz[t] : 0;
+    bool before = tile && P.nz_rowptr[r] < p0;
+    int row = 0, row_end, row_begin = 0;
+    int next_row = 0, next_end = 0x7fffffff, far_row = 0, far_end = 0x7fffffff;
     raw own_a[NV], own_b[NV], pre_a[NV], pre_b[NV];
     float own_lse = 0.f, pre_lse = 0.f;
-    auto prefetch_owner = [&]() {
-        load_row(P.own_a, next_row, true, pre_a);
-        if (MODE != kFwd) load_row(P.own_b, next_row, true, pre_b);
-        if (MODE == kDQ) pre_lse = P.lse[int64_t(next_row) * P.heads * 2 + stat_col];
+    auto load_owner = [&](int id, raw (&a)[NV], raw (&b)[NV], float &lse) {
+        load_row(P.own_a, id, a);
+        if (MODE != kFwd) load_row(P.own_b, id, b);
+        if (MODE == kDQ) lse = P.lse[int64_t(id) * P.heads * 2 + stat_col] * kLog2e;
     };
-    prefetch_owner();
-
-    // kFwd: sums of alpha v for the own and the other map; kDQ: A, B; kDKV: dk, dv
-    float acc[2][NV][VEC];
-    float m = 0.f, sum = 0.f, ref = 0.f;  // kFwd: maximum, sum; kDQ: sum of alpha, D', c
-    float dsum = 0.f;
-    bool open = false, first = false;
-
-    // adds the subs' acc and sums (kFwd: first to one maximum)
-    auto join_stats = [&]() {
-        if (MODE == kFwd) {
-            float M = m;
-            for (int o = sub_lanes; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-            const float f = ex2(m - (M == -INFINITY ? 0.f : M));
-            const float g = __shfl_xor_sync(kAll, f, DL);
-            sum *= f;
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) acc[0][k][v] *= f, acc[1][k][v] *= g;
-            m = M;
-        }
-        for (int o = sub_lanes; o < 32; o <<= 1) {
-            sum += __shfl_xor_sync(kAll, sum, o);
-            if (MODE == kDQ) dsum += __shfl_xor_sync(kAll, dsum, o);
+    auto meta = [&](int i, int &id, int &end) {  // row i of the rows with edges, if there is one
+        if (i < P.n_nz) {
+            id = __ldg(P.nz_rows + i);
+            end = int(__ldg(P.nz_rowptr + i + 1) - p0);
         }
     };
-    auto join = [&](float (&a)[NV][VEC]) {
-        for (int o = sub_lanes; o < 32; o <<= 1)
+    meta(r, row, row_end);
+    if (!tile) row_end = 0x7fffffff;
+    meta(r + 1, next_row, next_end);
+    meta(r + 2, far_row, far_end);
+    load_owner(row, own_a, own_b, own_lse);
+    load_owner(next_row, pre_a, pre_b, pre_lse);
+    if (tile) {
+        // the owner rows of the tile's further rows into L2: where rows are
+        // short, one opens every few positions
+        const int n = int(t + 1 < P.n_tiles ? P.tile_nz[t + 1] : P.n_nz - 1) - r;  // rows after the first
+        const int bytes = (P.heads - h0 < head_slots ? P.heads - h0 : head_slots) * 2 * P.d * int(sizeof(T));
+        for (int i = 2 + (lane & (group_lanes - 1)); i <= n; i += group_lanes) {
+            const int64_t at = (int64_t(P.nz_rows[r + i]) * P.H + int64_t(h0) * 2 * P.d) * int64_t(sizeof(T));
+            for (int o = 0; o < bytes; o += 128) {
+                prefetch_l2(static_cast<const char *>(P.own_a) + at + o);
+                if (MODE != kFwd) prefetch_l2(static_cast<const char *>(P.own_b) + at + o);
+            }
+        }
+    }
+
+    // kFwd: sums of p v for the own and the other map; kDQ: A, B; kDKV: dk, dv
+    Sums<VEC> acc[2][NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) acc[0][k].zero(), acc[1][k].zero();
+    float m = 0.f;            // kFwd: the reference of exp2(x - m); kDQ: c, the row's first da
+    float sum = 0.f;          // of exp2(x - m), or of alpha
+    float dsum = 0.f;         // kDQ: D'
+    bool first = true;        // the next position opens a row
+
+    // ------------------------------------------------------------ the ring of gathered rows
+    unsigned char *const ring = ring_mem[threadIdx.x >> 5];
+    if (RING) {  // pieces that no copy fills stay 0
+#pragma unroll
+        for (int s = 0; s < 4 * U; ++s)
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) a[k][v] += __shfl_xor_sync(kAll, a[k][v], o);
+                if (!ok[k]) *reinterpret_cast<raw *>(ring + (s * NV + k) * 32 * PIECE + lane * PIECE) = F::zero();
+    }
+    const int32_t *const col = P.col + p0;
+    const int last_unit = len > 0 ? (len - 1) & ~(U - 1) : 0;
+    // every group's tile is whole, with three units of positions behind it
+    const bool inner = __all_sync(kAll, tile && p0 + P.T + 3 * U <= P.E);
+    struct Ids {
+        int id[U];
     };
+    auto load_ids = [&](int p) {  // the gathered rows of positions p .. p + U - 1 (p a multiple of U)
+        Ids q;
+        const int32_t *at = col + (inner || p < last_unit ? p : last_unit);
+        if constexpr (U == 4) {
+            const int4 v = __ldg(reinterpret_cast<const int4 *>(at));
+            q.id[0] = v.x, q.id[1] = v.y, q.id[2] = v.z, q.id[3] = v.w;
+        } else if constexpr (U == 2) {
+            const int2 v = __ldg(reinterpret_cast<const int2 *>(at));
+            q.id[0] = v.x, q.id[1] = v.y;
+        } else {
+            q.id[0] = __ldg(at);
+        }
+        if (!inner) {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (p + i >= len) q.id[i] = 0;
+        }
+        return q;
+    };
+    const char *const nbr_a = static_cast<const char *>(P.nbr_a) + size_t(col0) * sizeof(T);
+    const char *const nbr_b = static_cast<const char *>(P.nbr_b) + size_t(col0) * sizeof(T);
+    const float2 *const nbr_st = P.stat + stat_col;
+    const uint32_t row_bytes = uint32_t(P.H) * uint32_t(sizeof(T));
+    const uint32_t stat_row = 2 * uint32_t(P.heads);
+    auto fetch = [&](uint32_t at, int id, int s) {  // into position s of the unit at `at`
+        const char *a = nbr_a + uint64_t(uint32_t(id)) * row_bytes;
+        const char *b = nbr_b + uint64_t(uint32_t(id)) * row_bytes;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (ok[k]) {
+                copy_async<PIECE>(at + s * kPosBytes + k * 32 * PIECE, a + k * DL * PIECE);
+                copy_async<PIECE>(at + s * kPosBytes + kRowBytes + k * 32 * PIECE, b + k * DL * PIECE);
+            }
+    };
+    const uint32_t ring_at = smem_addr(ring) + lane * PIECE;
+    const uint32_t stat_at = smem_addr(ring) + kRing + lane * 8;
+    auto fetch_unit = [&](int parity, const Ids &q) {
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            fetch(ring_at + parity * U * kPosBytes, q.id[s], s);
+            if (MODE == kDKV)
+                copy_async<8>(stat_at + (parity * U + s) * 32 * 8, nbr_st + uint64_t(uint32_t(q.id[s])) * stat_row);
+        }
+        cp_async_commit();
+    };
+    auto read = [&](int parity, int s, const Ids &q, raw (&a)[NV], raw (&b)[NV], float2 &st) {
+        if constexpr (RING) {
+            const unsigned char *at = ring + lane * PIECE + (parity * U + s) * kPosBytes;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                a[k] = *reinterpret_cast<const raw *>(at + k * 32 * PIECE);
+                b[k] = *reinterpret_cast<const raw *>(at + kRowBytes + k * 32 * PIECE);
+            }
+            if (MODE == kDKV) st = *reinterpret_cast<const float2 *>(ring + kRing + ((parity * U + s) * 32 + lane) * 8);
+        } else {
+            int id = q.id[0];
+#pragma unroll
+            for (int i = 1; i < U; ++i) id = s == i ? q.id[i] : id;
+            const T *pa = reinterpret_cast<const T *>(nbr_a + uint64_t(uint32_t(id)) * row_bytes);
+            const T *pb = reinterpret_cast<const T *>(nbr_b + uint64_t(uint32_t(id)) * row_bytes);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                a[k] = ok[k] ? F::load(pa + k * DL * VEC) : F::zero();
+                b[k] = ok[k] ? F::load(pb + k * DL * VEC) : F::zero();
+            }
+            if (MODE == kDKV) st = __ldg(nbr_st + uint64_t(uint32_t(id)) * stat_row);
+        }
+    };
+
     // the open row's partial of this tile
     auto write_slot = [&](int64_t s) {
-        join_stats();
-        join(acc[0]);
-        join(acc[1]);
-        if (sub != 0 || !live) return;
+        if (!live) return;
         float *base = P.partial + s * P.slot;
         const int which = MODE == kFwd ? map : 0;  // kFwd: maps in order, whichever is the lane's own
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            float *p = base + int64_t(a ^ which) * P.H + col0;
+            float *p = base + (a ^ which) * P.H + col0;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
+                if (ok[k]) {
+                    float v[VEC];
+                    acc[a][k].get(v);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    if (ok[k]) p[k * DL * VEC + v] = acc[a][k][v];
+                    for (int i = 0; i < VEC; ++i) p[k * DL * VEC + i] = v[i];
+                }
         }
         if (MODE != kDKV && l == 0) {
-            float *q = base + 2 * int64_t(P.H) + stat_col;
+            float *q = base + 2 * P.H + stat_col;
             q[0] = m;
             q[2 * P.heads] = sum;
             if (MODE == kDQ) q[4 * P.heads] = dsum;
         }
     };
-    auto finish_row = [&]() {
+    // writes the rows that end before position pos and opens the next ones (all lanes call it)
+    auto end_rows = [&](bool ends, int pos) {
+        float own_w = 0.f, other_w = 0.f;
+        if (MODE == kFwd) {
+            own_w = sign * __fdividef(P.drop.scale, sum);  // (sum below 2^71)
+            other_w = __shfl_xor_sync(kAll, own_w, DL);
+        }
+        if (!ends) return;
         if (before) {  // continued from the previous tile
             write_slot(2 * t);
             before = false;
-            return;
-        }
-        join_stats();
-        if (MODE == kFwd) {
-            const float inv = P.drop.scale / sum;
-            const float own_w = sign * inv;
-            const float other_w = __shfl_xor_sync(kAll, own_w, DL);
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) acc[0][k][v] = fmaf(acc[0][k][v], own_w, acc[1][k][v] * other_w);
-            join(acc[0]);
-            if (sub == 0) {
-                store_row(P.out_a, row, acc[0]);
-                if (live && l == 0) P.lse_out[int64_t(row) * P.heads * 2 + stat_col] = (m + log2f(sum)) * kLn2;
-            }
-        } else if (MODE == kDQ) {
-            const float w = sign * P.scale;
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) acc[0][k][v] = w * fmaf(-dsum, acc[1][k][v], acc[0][k][v]);
-            join(acc[0]);
-            if (sub == 0) {
-                store_row(P.out_a, row, acc[0]);
-                if (live && l == 0) P.stat[int64_t(row) * P.heads * 2 + stat_col] = make_float2(own_lse, ref + dsum);
-            }
         } else {
-            join(acc[0]);
-            join(acc[1]);
-            if (sub == 0) {
-                store_row(P.out_a, row, acc[0]);
-                store_row(P.out_b, row, acc[1]);
+            const float w = sign * P.scale;
+            const int64_t at = int64_t(row) * P.H + col0;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float u[VEC], v[VEC];
+                acc[0][k].get(u);
+                acc[1][k].get(v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (MODE == kFwd) u[i] = fmaf(u[i], own_w, v[i] * other_w);
+                    if (MODE == kDQ) u[i] = w * fmaf(-dsum, v[i], u[i]);
+                }
+                if (ok[k]) {
+                    F::store(static_cast<T *>(P.out_a) + at + k * DL * VEC, u);
+                    if (MODE == kDKV) F::store(static_cast<T *>(P.out_b) + at + k * DL * VEC, v);
+                }
+            }
+            if (live && l == 0) {
+                const int64_t c = int64_t(row) * P.heads * 2 + stat_col;
+                if (MODE == kFwd) P.lse_out[c] = (m + log2f(sum)) * kLn2;
+                if (MODE == kDQ) P.stat[c] = make_float2(own_lse, m + dsum);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            own_a[k] = pre_a[k];
+            if (MODE != kFwd) own_b[k] = pre_b[k];
+            acc[0][k].zero();
+            acc[1][k].zero();
+        }
+        own_lse = pre_lse;
+        sum = dsum = 0.f;
+        first = true;
+        row = next_row;
+        row_end = next_end;
+        row_begin = pos;
+        next_row = far_row;
+        next_end = far_end;
+        ++r;
+        load_owner(next_row, pre_a, pre_b, pre_lse);
+        meta(r + 2, far_row, far_end);
+    };
+    // n positions of the unit, from s on, none of which opens a row but the
+    // first; in the group's range where valid (kFwd, kDQ: -inf and 0 outside)
+    auto take = [&](auto count, int parity, int s0, const Ids &q, uint32_t kept, bool valid) {
+        constexpr int n = decltype(count)::value;
+        raw a[n][NV], b[n][NV];
+        float2 st[n];
+        float x[n], da[n];
+#pragma unroll
+        for (int s = 0; s < n; ++s) read(parity, s0 + s, q, a[s], b[s], st[s]);
+#pragma unroll
+        for (int s = 0; s < n; ++s) {
+            x[s] = da[s] = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) x[s] = F::dot(own_a[k], a[s][k], x[s]);
+            x[s] = group_sum<DL>(x[s]);
+            if (MODE != kFwd) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) da[s] = F::dot(own_b[k], b[s][k], da[s]);
+                da[s] = group_sum<HL>(da[s]);
+                if (DROP) da[s] = kept >> s & 1u ? da[s] * P.drop.scale : 0.f;
+            }
+        }
+        if (MODE == kFwd) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int s = 0; s < n; ++s) {
+                x[s] = valid ? x[s] * P.c2 : -INFINITY;
+                top = fmaxf(top, x[s]);
+            }
+            if (first) m = fmaxf(x[0], -3.402823466e38f);  // never -inf: exp2(-inf - m) is 0
+            if (__any_sync(kAll, top > m + kSlack)) {
+                top = fmaxf(m, top);
+                const float f = ex2(m - top);
+                const float g = __shfl_xor_sync(kAll, f, DL);
+                sum *= f;
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    float u[VEC], v[VEC];
+                    acc[0][k].get(u);
+                    acc[1][k].get(v);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) u[i] *= f, v[i] *= g;
+                    acc[0][k].set(u);
+                    acc[1][k].set(v);
+                }
+                m = top;
+            }
+        }
+        if (MODE == kDQ && first) m = da[0];
+        first = false;
+#pragma unroll
+        for (int s = 0; s < n; ++s) {
+            float f0, f1;  // the factors of acc[0] and acc[1]
+            if (MODE == kFwd) {
+                f0 = ex2(x[s] - m);
+                sum += f0;
+                f1 = __shfl_xor_sync(kAll, f0, DL);
+            } else if (MODE == kDQ) {
+                f1 = ex2(fmaf(x[s], P.c2, -own_lse));
+                f0 = f1 * (da[s] - m);
+                if (!valid) f0 = f1 = 0.f;
+                sum += f1;
+                dsum += f0;
+            } else {
+                const float p = sign * ex2(fmaf(x[s], P.c2, -st[s].x));
+                f1 = p + __shfl_xor_sync(kAll, p, DL);
+                f0 = P.scale * p * (da[s] - st[s].y);
+                if (!valid) f0 = f1 = 0.f;
+                if (DROP) f1 = kept >> s & 1u ? f1 * P.drop.scale : 0.f;
+            }
+            const uint64_t ff0 = Sums<VEC>::pair(f0, f0), ff1 = Sums<VEC>::pair(f1, f1);
+            // what is dropped (kFwd) or outside may hold infinities
+            const bool use = valid && (!DROP || MODE != kFwd || (kept >> s & 1u));
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float va[VEC], vb[VEC];
+                if (MODE != kFwd) F::unpack_if(a[s][k], use, va);
+                if (MODE != kDQ) F::unpack_if(b[s][k], use, vb);
+                if (MODE == kFwd) acc[0][k].add(ff0, vb), acc[1][k].add(ff1, vb);
+                if (MODE == kDQ) acc[0][k].add(ff0, va), acc[1][k].add(ff1, va);
+                if (MODE == kDKV) acc[0][k].add(ff0, va), acc[1][k].add(ff1, vb);
             }
         }
     };
 
-    int cid_next = lane < len ? __ldg(col + lane) : 0;
-    for (int b0 = 0; b0 < len; b0 += 32) {
-        const int cid = cid_next;
-        cid_next = b0 + 32 + lane < len ? __ldg(col + b0 + 32 + lane) : 0;
-        uint32_t bits = 0xffffffffu;
-        if (P.drop.on && b0 + lane < len) {
-            const int64_t e = P.order[p0 + b0 + lane];
+    Ids ids = load_ids(0);
+    if (RING) {
+        fetch_unit(0, ids);
+        ids = load_ids(U);
+        fetch_unit(1, ids);
+        ids = load_ids(2 * U);
+    }
+    // keep bits of this lane's head: of `batch` positions from mask_at on
+    const int gl = lane & (group_lanes - 1);
+    const int group0 = lane & ~(group_lanes - 1);
+    const int batch = group_lanes > U ? group_lanes : U;
+    uint32_t bits = 0xffffffffu;
+    int edge = DROP && gl < len ? __ldg(P.order + p0 + gl) : 0;
+    int stop = row_end < len || !tile ? row_end : len;  // the end of what is taken without a look
+    for (int pos = 0; pos < steps; pos += U) {
+        const int parity = pos / U & 1;
+        if (DROP && (pos & (batch - 1)) == 0) {  // a position per lane, then a word per head
             const int count = P.heads - h0 < head_slots ? P.heads - h0 : head_slots;
-            bits = keep_bits(uint64_t(e) * P.heads + h0, count, P.drop);
+            bits = 0;
+            for (int o = 0; o < batch; o += group_lanes) {
+                const uint32_t k = keep_bits<1>(uint64_t(uint32_t(edge)) * uint32_t(P.heads) + uint32_t(h0), count, P.drop);
+                for (int h = 0; h < head_slots; ++h) {
+                    const uint32_t w = __ballot_sync(kAll, k >> h & 1u) >> group0;
+                    if (h == hs) bits |= (group_lanes == 32 ? w : w & ((1u << group_lanes) - 1u)) << o;
+                }
+                const int ahead = pos + o + group_lanes + gl;
+                edge = ahead < len ? __ldg(P.order + p0 + ahead) : 0;
+            }
         }
-        const int b1 = b0 + 32 < len ? b0 + 32 : len;
-        int pos = b0;
-        while (pos < b1) {
-            if (!open) {
-                row = next_row;
-                row_end = next_end;
-#pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    own_a[k] = pre_a[k];
-                    if (MODE != kFwd) own_b[k] = pre_b[k];
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) acc[0][k][v] = acc[1][k][v] = 0.f;
-                }
-                if (MODE == kDQ) own_lse = pre_lse * kLog2e;
-                m = MODE == kFwd ? -INFINITY : 0.f;
-                sum = dsum = 0.f;
-                open = first = true;
-                if (r + 1 < P.n_nz) {
-                    next_row = P.nz_rows[r + 1];
-                    next_end = int(P.nz_rowptr[r + 2] - p0);
-                    prefetch_owner();
-                }
+        if (RING) cp_async_wait<1>();
+        // the whole unit at once where no group's row ends inside it
+        const bool whole = __all_sync(kAll, stop >= pos + U);
+        if (whole) take(std::integral_constant<int, U>(), parity, 0, ids, bits, true);
+        for (int s = whole ? U - 1 : 0; s < U; ++s) {
+            if (!whole) take(std::integral_constant<int, 1>(), parity, s, ids, bits >> s, pos + s < len);
+            const bool ends = pos + s + 1 == row_end;
+            if (__any_sync(kAll, ends)) {
+                end_rows(ends, pos + s + 1);
+                stop = row_end < len || !tile ? row_end : len;
             }
-            const int seg_end = row_end < b1 ? row_end : b1;
-            for (int i = pos; i < seg_end; i += nsub * U) {
-                raw na[U][NV], nb[U][NV];
-                float2 st[U];
-                bool valid[U];
-                uint32_t kept[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int j = i + u * nsub + sub;
-                    valid[u] = j < seg_end;
-                    const int64_t c = __shfl_sync(kAll, cid, j & 31);
-                    kept[u] = P.drop.on ? __shfl_sync(kAll, bits, j & 31) >> hs & 1u : 1u;
-                    load_row(P.nbr_a, c, valid[u], na[u]);
-                    load_row(P.nbr_b, c, valid[u], nb[u]);
-                    if (MODE == kDKV) st[u] = valid[u] ? __ldg(P.stat + c * P.heads * 2 + stat_col) : make_float2(0.f, 0.f);
-                }
-                float x[U], da[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    x[u] = da[u] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < NV; ++k) x[u] = F::dot(own_a[k], na[u][k], x[u]);
-                    x[u] = group_sum<DL>(x[u]);
-                    if (MODE != kFwd) {
-#pragma unroll
-                        for (int k = 0; k < NV; ++k) da[u] = F::dot(own_b[k], nb[u][k], da[u]);
-                        da[u] = group_sum<HL>(da[u]);
-                        da[u] = kept[u] ? da[u] * P.drop.scale : 0.f;
-                    }
-                }
-                if (MODE == kFwd) {
-                    float top = m;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        x[u] = valid[u] ? x[u] * P.c2 : -INFINITY;
-                        top = fmaxf(top, x[u]);
-                    }
-                    const float base = top == -INFINITY ? 0.f : top;
-                    if (__any_sync(kAll, top > m)) {
-                        const float f = ex2(m - base);
-                        const float g = __shfl_xor_sync(kAll, f, DL);
-                        sum *= f;
-#pragma unroll
-                        for (int k = 0; k < NV; ++k)
-#pragma unroll
-                            for (int v = 0; v < VEC; ++v) acc[0][k][v] *= f, acc[1][k][v] *= g;
-                        m = top;
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        float p = ex2(x[u] - base);
-                        sum += p;
-                        p = kept[u] ? p : 0.f;
-                        const float q = __shfl_xor_sync(kAll, p, DL);
-#pragma unroll
-                        for (int k = 0; k < NV; ++k) {
-                            float vv[VEC];
-                            F::unpack(nb[u][k], vv);
-#pragma unroll
-                            for (int v = 0; v < VEC; ++v) {
-                                acc[0][k][v] = fmaf(p, vv[v], acc[0][k][v]);
-                                acc[1][k][v] = fmaf(q, vv[v], acc[1][k][v]);
-                            }
-                        }
-                    }
-                } else if (MODE == kDQ) {
-                    if (first) {  // the row's first edge in this tile: edge 0 of sub 0
-                        ref = __shfl_sync(kAll, da[0], lane & (sub_lanes - 1));
-                        m = ref;
-                        first = false;
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const float p = valid[u] ? ex2(fmaf(x[u], P.c2, -own_lse)) : 0.f;
-                        const float q = valid[u] ? p * (da[u] - ref) : 0.f;
-                        sum += p;
-                        dsum += q;
-#pragma unroll
-                        for (int k = 0; k < NV; ++k) {
-                            float vv[VEC];
-                            F::unpack(na[u][k], vv);
-#pragma unroll
-                            for (int v = 0; v < VEC; ++v) {
-                                acc[0][k][v] = fmaf(q, vv[v], acc[0][k][v]);
-                                acc[1][k][v] = fmaf(p, vv[v], acc[1][k][v]);
-                            }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const float p = valid[u] ? sign * ex2(fmaf(x[u], P.c2, -st[u].x)) : 0.f;
-                        const float both = p + __shfl_xor_sync(kAll, p, DL);
-                        const float ds = valid[u] ? P.scale * p * (da[u] - st[u].y) : 0.f;
-                        const float w = kept[u] ? both * P.drop.scale : 0.f;
-#pragma unroll
-                        for (int k = 0; k < NV; ++k) {
-                            float va[VEC], vb[VEC];
-                            F::unpack(na[u][k], va);
-                            F::unpack(nb[u][k], vb);
-#pragma unroll
-                            for (int v = 0; v < VEC; ++v) {
-                                acc[0][k][v] = fmaf(ds, va[v], acc[0][k][v]);
-                                acc[1][k][v] = fmaf(w, vb[v], acc[1][k][v]);
-                            }
-                        }
-                    }
-                }
-            }
-            pos = seg_end;
-            if (seg_end == row_end) {
-                finish_row();
-                open = false;
-                ++r;
-            }
+        }
+        if (DROP) bits >>= U;
+        if (RING) {
+            fetch_unit(parity, ids);
+            ids = load_ids(pos + 3 * U);
+        } else {
+            ids = load_ids(pos + U);
         }
     }
-    if (open) write_slot(before ? 2 * t : 2 * t + 1);
+    if (RING) cp_async_wait<0>();
+    if (row_begin < len) write_slot(before ? 2 * t : 2 * t + 1);  // the row open at the tile's end
 }
 
 // Rows cut by tile boundaries: the partials of slot 2 first + 1 and of the
-// slots 2t of tiles first + 1 .. last, added in tile order.  One block per
-// row for the rows cut into many tiles (listed first; its threads split into
-// stripes of columns, each taking every stripes-th slot, then the stripes are
-// added in order), one warp for every other row.
-constexpr int kFixThreads = 256;
+// slots 2t of tiles first + 1 .. last.  A row cut into many tiles (those are
+// listed first) takes a block: a warp per (head, map) reduces its statistics
+// over the slots, then stripes of threads add every stripes-th slot's columns
+// and the stripes are added in order.  Every other row takes a warp, which
+// adds the slots in order.  All orders are fixed by the graph and the sizes.
+constexpr int kFixThreads = 512;
 
 struct FixParams {
     const int4 *spans;
@@ -445,163 +555,172 @@ struct FixParams {
     float scale, drop_scale;
 };
 
-// The sums over slots first, first + step, ... of one column: kFwd weights
-// the maps' sums by exp2(m - M), kDQ shifts A by (c - C) B.
-template <int MODE>
-__device__ __forceinline__ float2 fix_column(const FixParams &P, int64_t s0, int64_t t0, int n, int first, int step,
-                                             int c, float M1, float M2) {
-    const int head = c / (2 * P.d), map = c / P.d & 1;
-    float2 a = make_float2(0.f, 0.f);
-    for (int i = first; i < n; i += step) {
-        const float *b = P.partial + (i == 0 ? s0 : 2 * (t0 + i)) * P.slot;
-        const float u = b[c], v = b[P.H + c];
-        const float *q = b + 2 * int64_t(P.H) + 2 * head;
-        if (MODE == kFwd) {
-            a.x = fmaf(u, ex2(q[0] - M1), a.x);
-            a.y = fmaf(v, ex2(q[1] - M2), a.y);
-        } else if (MODE == kDQ) {
-            a.x += fmaf(q[map] - M1, v, u);  // M1: the row's c
-            a.y += v;
-        } else {
-            a.x += u;
-            a.y += v;
+struct Span {  // one cut row's slots, 0 .. n - 1
+    const float *first, *rest;
+    int64_t step;
+    int n;
+    __device__ __forceinline__ Span(const FixParams &P, const int4 &sp)
+        : first(P.partial + (2 * int64_t(sp.y) + 1) * P.slot), rest(P.partial + 2 * int64_t(sp.y) * P.slot),
+          step(2 * P.slot), n(sp.z - sp.y + 1) {}
+    __device__ __forceinline__ const float *operator[](int i) const { return i == 0 ? first : rest + i * step; }
+};
+
+// CV columns from c on (of one map) over the slots i0, i0 + step, ...: a, b
+// are the two sums.  kFwd weights them by exp2(m - M) of their maps, kDQ adds
+// (c - C) B to A, where ref = (M1, M2) or (C, -).
+template <int MODE, int CV>
+__device__ __forceinline__ void fix_columns(const FixParams &P, const Span &S, int i0, int step, int c, int q0, int map,
+                                            float2 ref, float (&a)[CV], float (&b)[CV]) {
+#pragma unroll
+    for (int v = 0; v < CV; ++v) a[v] = b[v] = 0.f;
+#pragma unroll 4
+    for (int i = i0; i < S.n; i += step) {
+        const float *p = S[i] + c;
+        float u[CV], w[CV];
+        Frag<float, CV>::unpack(Frag<float, CV>::load(p), u);
+        Frag<float, CV>::unpack(Frag<float, CV>::load(p + P.H), w);
+        float f = 1.f, g = 1.f, shift = 0.f;
+        if (MODE == kFwd) f = ex2(S[i][q0] - ref.x), g = ex2(S[i][q0 + 1] - ref.y);
+        if (MODE == kDQ) shift = S[i][q0 + map] - ref.x;
+#pragma unroll
+        for (int v = 0; v < CV; ++v) {
+            a[v] = MODE == kDQ ? a[v] + fmaf(shift, w[v], u[v]) : fmaf(f, u[v], a[v]);
+            b[v] = fmaf(g, w[v], b[v]);
         }
     }
-    return a;
 }
 
-// Statistics of (head, map) index j over slots first, first + step, ...:
-// kFwd (M, L); kDQ (C, D' rebased to C).
-template <int MODE>
-__device__ __forceinline__ float2 fix_stats(const FixParams &P, int64_t s0, int64_t t0, int n, int j) {
-    const float *q0 = P.partial + 2 * int64_t(P.H) + j;
-    auto at = [&](int i) { return q0 + (i == 0 ? s0 : 2 * (t0 + i)) * P.slot; };
-    float2 a;
+// Statistics at index q of a slot: kFwd (M, L), kDQ (C, D' rebased to C), of
+// all slots (lanes = 1) or of one lane's share of a warp's.
+template <int MODE, bool WARP>
+__device__ __forceinline__ float2 fix_stats(const FixParams &P, const Span &S, int q) {
+    const int lane = WARP ? threadIdx.x & 31 : 0, step = WARP ? 32 : 1;
+    const int h2 = 2 * P.heads;
     if (MODE == kFwd) {
-        float M = -INFINITY;
-        for (int i = 0; i < n; ++i) M = fmaxf(M, at(i)[0]);
-        if (M == -INFINITY) M = 0.f;
+        float M = -3.402823466e38f;
+        for (int i = lane; i < S.n; i += step) M = fmaxf(M, S[i][q]);
+        if (WARP) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+        }
         float L = 0.f;
-        for (int i = 0; i < n; ++i) L = fmaf(at(i)[2 * P.heads], ex2(at(i)[0] - M), L);
-        a = make_float2(M, L);
-    } else {
-        const float C = at(0)[0];
-        float D = 0.f;
-        for (int i = 0; i < n; ++i) D += fmaf(at(i)[0] - C, at(i)[2 * P.heads], at(i)[4 * P.heads]);
-        a = make_float2(C, D);
+        for (int i = lane; i < S.n; i += step) L = fmaf(S[i][q + h2], ex2(S[i][q] - M), L);
+        return make_float2(M, WARP ? group_sum<32>(L) : L);
     }
-    return a;
+    const float C = S[0][q];
+    float D = 0.f;
+    for (int i = lane; i < S.n; i += step) D += fmaf(S[i][q] - C, S[i][q + h2], S[i][q + 2 * h2]);
+    return make_float2(C, WARP ? group_sum<32>(D) : D);
 }
 
-template <typename T, int MODE>
-__device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c, float2 a, float2 s1, float2 s2) {
-    const int head = c / (2 * P.d), map = c / P.d & 1;
+template <typename T, int MODE, int CV>
+__device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c, int head, int map, float2 s1, float2 s2,
+                                          float (&a)[CV], float (&b)[CV]) {
     const float lam = P.lam[head];
-    float y[1];
-    if (MODE == kFwd) {
-        y[0] = P.drop_scale * (a.x / s1.y - lam * (a.y / s2.y));
-    } else if (MODE == kDQ) {
-        y[0] = (map ? -lam : 1.f) * P.scale * fmaf(-s1.y, a.y, a.x);  // s1: this map's (C, D')
-    } else {
-        y[0] = a.x;
+    float f = 1.f, g = 0.f;
+    if (MODE == kFwd) f = __fdividef(P.drop_scale, s1.y), g = -lam * __fdividef(P.drop_scale, s2.y);
+    if (MODE == kDQ) f = (map ? -lam : 1.f) * P.scale, g = -s1.y * f;  // s1: this map's (C, D')
+    T *out = static_cast<T *>(P.out_a) + row * P.H + c;
+    if (MODE != kDKV) {
+#pragma unroll
+        for (int v = 0; v < CV; ++v) a[v] = fmaf(f, a[v], g * b[v]);
     }
-    Frag<T, 1>::store(static_cast<T *>(P.out_a) + row * P.H + c, y);
-    if (MODE == kDKV) {
-        y[0] = a.y;
-        Frag<T, 1>::store(static_cast<T *>(P.out_b) + row * P.H + c, y);
+    Frag<T, CV>::store(out, a);
+    if (MODE == kDKV) Frag<T, CV>::store(static_cast<T *>(P.out_b) + row * P.H + c, b);
+    if (MODE != kDKV && c % P.d == 0) {  // the map's statistics, once
+        const int64_t k = (row * P.heads + head) * 2 + map;
+        const float2 s = MODE == kFwd && map ? s2 : s1;
+        if (MODE == kFwd) P.lse_out[k] = (s.x + log2f(s.y)) * kLn2;
+        if (MODE == kDQ) P.stat[k] = make_float2(P.lse[k] * kLog2e, s.x + s.y);
     }
-}
-template <int MODE>
-__device__ __forceinline__ void fix_store_stats(const FixParams &P, int64_t row, int j, float2 s) {
-    const int64_t k = row * P.heads * 2 + j;
-    if (MODE == kFwd) P.lse_out[k] = (s.x + log2f(s.y)) * kLn2;
-    if (MODE == kDQ) P.stat[k] = make_float2(P.lse[k] * kLog2e, s.x + s.y);
 }
 
-template <typename T, int MODE>
+template <typename T, int MODE, int CV>
 __global__ void __launch_bounds__(kFixThreads) k_diff_fixup(const FixParams P) {
-    __shared__ float2 stats[2 * kMaxHeads];  // long rows: per (head, map)
-    __shared__ float2 red[kFixThreads];
+    __shared__ float2 stats[MODE == kDKV ? 1 : 2 * kMaxHeads];  // long rows: per (head, map)
+    __shared__ float red[2 * CV][kFixThreads];
+    const int q_at = 2 * P.H;  // a slot's statistics
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x < P.n_long) {
         const int4 sp = P.spans[blockIdx.x];
-        const int n = sp.z - sp.y + 1;
-        const int64_t s0 = 2 * int64_t(sp.y) + 1, t0 = sp.y;
+        const Span S(P, sp);
         if (MODE != kDKV) {
-            for (int j = threadIdx.x; j < 2 * P.heads; j += kFixThreads) {
-                stats[j] = fix_stats<MODE>(P, s0, t0, n, j);
-                fix_store_stats<MODE>(P, sp.x, j, stats[j]);
+            for (int j = warp; j < 2 * P.heads; j += kFixThreads / 32) {
+                const float2 s = fix_stats<MODE, true>(P, S, q_at + j);
+                if (lane == 0) stats[j] = s;
             }
             __syncthreads();
         }
         int cols = 32;
-        while (cols < P.H && cols < kFixThreads) cols <<= 1;
-        const int stripes = kFixThreads / cols;
-        const int stripe = threadIdx.x / cols;
-        for (int c0 = 0; c0 < P.H; c0 += cols) {
-            const int c = c0 + threadIdx.x % cols;
-            float2 s1 = make_float2(0.f, 1.f), s2 = s1, a = make_float2(0.f, 0.f);
+        while (cols * CV < P.H && cols < kFixThreads) cols <<= 1;
+        const int stripes = kFixThreads / cols, stripe = threadIdx.x / cols, tc = threadIdx.x % cols;
+        for (int c0 = 0; c0 < P.H; c0 += cols * CV) {
+            const int c = c0 + tc * CV;
+            const int head = c / (2 * P.d), map = c / P.d & 1;
+            float a[CV], b[CV];
+            float2 s1 = make_float2(0.f, 1.f), s2 = s1;
             if (c < P.H) {
-                if (MODE == kFwd) s1 = stats[c / (2 * P.d) * 2], s2 = stats[c / (2 * P.d) * 2 + 1];
-                if (MODE == kDQ) s1 = stats[c / P.d];
-                a = fix_column<MODE>(P, s0, t0, n, stripe, stripes, c, s1.x, s2.x);
+                if (MODE == kFwd) s1 = stats[2 * head], s2 = stats[2 * head + 1];
+                if (MODE == kDQ) s1 = stats[2 * head + map];
+                fix_columns<MODE, CV>(P, S, stripe, stripes, c, q_at + 2 * head, map, make_float2(s1.x, s2.x), a, b);
+#pragma unroll
+                for (int v = 0; v < CV; ++v) red[v][threadIdx.x] = a[v], red[CV + v][threadIdx.x] = b[v];
             }
-            red[threadIdx.x] = a;
             __syncthreads();
             if (stripe == 0 && c < P.H) {
-                for (int k = 1; k < stripes; ++k) {
-                    const float2 b = red[k * cols + threadIdx.x];
-                    a.x += b.x;
-                    a.y += b.y;
-                }
-                fix_store<T, MODE>(P, sp.x, c, a, s1, s2);
+                for (int k = 1; k < stripes; ++k)
+#pragma unroll
+                    for (int v = 0; v < CV; ++v) a[v] += red[v][k * cols + tc], b[v] += red[CV + v][k * cols + tc];
+                fix_store<T, MODE, CV>(P, sp.x, c, head, map, s1, s2, a, b);
             }
             __syncthreads();
         }
         return;
     }
-    const int lane = threadIdx.x & 31;
-    const int64_t s = P.n_long + (int64_t(blockIdx.x) - P.n_long) * (kFixThreads / 32) + (threadIdx.x >> 5);
+    const int64_t s = P.n_long + (int64_t(blockIdx.x) - P.n_long) * (kFixThreads / 32) + warp;
     if (s >= P.n_span) return;
     const int4 sp = P.spans[s];
-    const int n = sp.z - sp.y + 1;
-    const int64_t s0 = 2 * int64_t(sp.y) + 1, t0 = sp.y;
-    for (int c = lane; c < P.H; c += 32) {
-        const int head = c / (2 * P.d);
+    const Span S(P, sp);
+    for (int c = lane * CV; c < P.H; c += 32 * CV) {
+        const int head = c / (2 * P.d), map = c / P.d & 1;
+        const int q = q_at + 2 * head;
         float2 s1 = make_float2(0.f, 1.f), s2 = s1;
-        if (MODE == kFwd) s1 = fix_stats<MODE>(P, s0, t0, n, 2 * head), s2 = fix_stats<MODE>(P, s0, t0, n, 2 * head + 1);
-        if (MODE == kDQ) s1 = fix_stats<MODE>(P, s0, t0, n, c / P.d);
-        fix_store<T, MODE>(P, sp.x, c, fix_column<MODE>(P, s0, t0, n, 0, 1, c, s1.x, s2.x), s1, s2);
-    }
-    if (MODE != kDKV)
-        for (int j = lane; j < 2 * P.heads; j += 32) fix_store_stats<MODE>(P, sp.x, j, fix_stats<MODE>(P, s0, t0, n, j));
-}
-
-// dlambda[h] = -sum over rows of D_2: block b sums rows b, b + blocks, ...
-// in fp64 (a row's threads fixed), then one block adds the blocks in order.
-constexpr int kLamBlocks = 148;
-
-__global__ void __launch_bounds__(256) k_diff_dlam(const float2 *__restrict__ stat, int64_t N, int heads,
-                                                   double *__restrict__ partial) {
-    __shared__ double red[256];
-    for (int h = 0; h < heads; ++h) {
-        double s = 0.0;
-        for (int64_t r = int64_t(blockIdx.x) * 256 + threadIdx.x; r < N; r += int64_t(gridDim.x) * 256)
-            s += double(stat[(r * heads + h) * 2 + 1].y);
-        red[threadIdx.x] = s;
-        __syncthreads();
-        for (int o = 128; o > 0; o >>= 1) {
-            if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-            __syncthreads();
-        }
-        if (threadIdx.x == 0) partial[int64_t(blockIdx.x) * heads + h] = red[0];
-        __syncthreads();
+        if (MODE == kFwd) s1 = fix_stats<MODE, false>(P, S, q), s2 = fix_stats<MODE, false>(P, S, q + 1);
+        if (MODE == kDQ) s1 = fix_stats<MODE, false>(P, S, q + map);
+        float a[CV], b[CV];
+        fix_columns<MODE, CV>(P, S, 0, 1, c, q, map, make_float2(s1.x, s2.x), a, b);
+        fix_store<T, MODE, CV>(P, sp.x, c, head, map, s1, s2, a, b);
     }
 }
-__global__ void k_diff_dlam_join(const double *__restrict__ partial, int blocks, int heads, float *__restrict__ dlam) {
-    for (int h = threadIdx.x; h < heads; h += blockDim.x) {
-        double s = 0.0;
-        for (int b = 0; b < blocks; ++b) s += partial[int64_t(b) * heads + h];
-        dlam[h] = float(-s);
+
+// dlambda[h] = -sum over rows of D_2, in fp64: a thread adds rows of one head
+// (the rows' stride is fixed), a block its threads, and a second launch of one
+// block the blocks.
+constexpr int kLamBlocks = 296;
+constexpr int kLamThreads = 256;
+
+template <bool LAST>
+__global__ void __launch_bounds__(kLamThreads) k_diff_dlam(const float2 *__restrict__ stat, int64_t N, int heads,
+                                                           double *__restrict__ partial, float *__restrict__ dlam) {
+    __shared__ double red[kLamThreads];
+    const int per = kLamThreads / heads, h = threadIdx.x % heads, g = threadIdx.x / heads;
+    double s = 0.0;
+    if (g < per) {
+#pragma unroll 4
+        for (int64_t r = int64_t(blockIdx.x) * per + g; r < N; r += int64_t(gridDim.x) * per)
+            s += LAST ? partial[r * heads + h] : double(stat[(r * heads + h) * 2 + 1].y);
+    }
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int n = per; n > 1;) {
+        const int half = (n + 1) / 2;
+        if (g < n - half) red[threadIdx.x] += red[threadIdx.x + half * heads];
+        n = half;
+        __syncthreads();
+    }
+    if (threadIdx.x < heads) {
+        if (LAST) dlam[h] = float(-red[h]);
+        else partial[int64_t(blockIdx.x) * heads + h] = red[h];
     }
 }
 
@@ -632,11 +751,14 @@ void launch_walk(DiffParams &P, cudaStream_t st) {
     int hb = 0;  // head slots: fill the warp, not beyond the heads
     while ((4 * DL << hb) <= 32 && (1 << hb) < P.heads) ++hb;
     P.hb_log2 = hb;
-    P.tile_blocks = unsigned((P.n_tiles + kWarps - 1) / kWarps);
+    const int tiles = kWarps * (32 / (2 * DL << hb));  // per block
+    P.tile_blocks = unsigned((P.n_tiles + tiles - 1) / tiles);
     const int64_t zero = (P.n_zero + kWarps * kZeroPerWarp - 1) / (kWarps * kZeroPerWarp);
     const unsigned y = unsigned((P.heads + (1 << hb) - 1) >> hb);
     const dim3 grid(unsigned(P.tile_blocks + zero), y);
-    if (grid.x > 0) k_diff_walk<T, VEC, DL, NV, MODE><<<grid, kWarps * 32, 0, st>>>(P);
+    if (grid.x == 0) return;
+    if (P.drop.on) k_diff_walk<T, VEC, DL, NV, MODE, true><<<grid, kWarps * 32, 0, st>>>(P);
+    else k_diff_walk<T, VEC, DL, NV, MODE, false><<<grid, kWarps * 32, 0, st>>>(P);
 }
 
 // Vectors per map n = d / VEC: the next power of two of lanes up to 16, then
@@ -697,8 +819,15 @@ void launch_fixup(const Direction &D, const DiffParams &P, int dtype, cudaStream
     F.scale = P.scale;
     F.drop_scale = P.drop.scale;
     const unsigned grid = unsigned(F.n_long + (F.n_span - F.n_long + kFixThreads / 32 - 1) / (kFixThreads / 32));
-    if (dtype == AG_F32) k_diff_fixup<float, MODE><<<grid, kFixThreads, 0, st>>>(F);
-    else k_diff_fixup<bf16_t, MODE><<<grid, kFixThreads, 0, st>>>(F);
+    // four columns a thread where maps and rows divide so (slots are 16-byte aligned) and the outputs' addresses do
+    const bool four = P.d % 4 == 0 && (uintptr_t(P.out_a) | uintptr_t(P.out_b)) % (dtype == AG_F32 ? 16 : 8) == 0;
+    if (dtype == AG_F32) {
+        if (four) k_diff_fixup<float, MODE, 4><<<grid, kFixThreads, 0, st>>>(F);
+        else k_diff_fixup<float, MODE, 1><<<grid, kFixThreads, 0, st>>>(F);
+    } else {
+        if (four) k_diff_fixup<bf16_t, MODE, 4><<<grid, kFixThreads, 0, st>>>(F);
+        else k_diff_fixup<bf16_t, MODE, 1><<<grid, kFixThreads, 0, st>>>(F);
+    }
 }
 
 void set_direction(DiffParams &P, const ag_graph *g, int dir) {
@@ -709,7 +838,7 @@ void set_direction(DiffParams &P, const ag_graph *g, int dir) {
     P.nz_rows = D.nz_rows;
     P.nz_rowptr = D.nz_rowptr;
     P.zero_rows = D.zero_rows;
-    P.n_nz = D.n_nz;
+    P.n_nz = int(D.n_nz);
     P.n_zero = g->N - D.n_nz;
     P.n_tiles = g->n_tiles;
     P.E = g->E;
@@ -835,10 +964,11 @@ int ag_diff_attn_backward(const ag_graph *g, const void *Q, const void *K, const
     launch_fixup<kDQ>(g->dir[0], P, dtype, st);
     // dlambda from the rows' D
     double *part = reinterpret_cast<double *>(scr + L.dlam);
-    const int64_t rows = (g->N + 255) / 256;
-    const int blocks = int(rows < kLamBlocks ? rows : kLamBlocks);
-    k_diff_dlam<<<blocks, 256, 0, st>>>(P.stat, g->N, int(heads), part);
-    k_diff_dlam_join<<<1, 256, 0, st>>>(part, blocks, int(heads), dlam);
+    const int64_t per = 8 * (kLamThreads / heads);  // rows that fill a block
+    const int64_t want = (g->N + per - 1) / per;
+    const int blocks = int(want < kLamBlocks ? want : kLamBlocks);
+    k_diff_dlam<false><<<blocks, kLamThreads, 0, st>>>(P.stat, g->N, int(heads), part, nullptr);
+    k_diff_dlam<true><<<1, kLamThreads, 0, st>>>(nullptr, blocks, int(heads), part, dlam);
     // dK and dV over the source rows
     set_direction(P, g, 1);
     P.own_a = K;

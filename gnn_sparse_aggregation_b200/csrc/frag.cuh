@@ -49,6 +49,21 @@ template <typename T, int VEC> struct Frag {
             }
         }
     }
+    // the features where `keep`, else zeros whatever they hold (bf16: the
+    // shift and the mask that unpack take the factor and the mask 0 instead)
+    static __device__ __forceinline__ void unpack_if(raw r, bool keep, float (&v)[VEC]) {
+        Bits b;
+        if (kBytes < 4) b.w[0] = 0u;
+        b.r = r;
+        if (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = keep ? __uint_as_float(b.w[i]) : 0.f;
+        } else {
+            const uint32_t up = keep ? 65536u : 0u, high = keep ? 0xffff0000u : 0u;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(i & 1 ? b.w[i / 2] & high : b.w[i / 2] * up);
+        }
+    }
     static __device__ __forceinline__ raw pack(const float (&v)[VEC]) {
         Bits b;
         if (sizeof(T) == 4) {
@@ -58,7 +73,8 @@ template <typename T, int VEC> struct Frag {
             b.w[0] = bf16_bits(v[0]);
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) b.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            for (int i = 0; i < VEC / 2; ++i)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b.w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
         }
         return b.r;
     }
@@ -83,6 +99,43 @@ template <typename T, int VEC> struct Frag {
         }
         return c;
     }
+};
+
+// VEC fp32 sums, in pairs where there are pairs: one fma.rn.f32x2 adds to two.
+template <int VEC> struct Sums {
+    static constexpr int kPairs = VEC / 2;
+    uint64_t s[kPairs];
+
+    static __device__ __forceinline__ uint64_t pair(float a, float b) {
+        uint64_t r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+        return r;
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) s[i] = 0ull;
+    }
+    __device__ __forceinline__ void add(uint64_t ff, const float (&v)[VEC]) {  // s += f v, ff = pair(f, f)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(s[i]) : "l"(ff), "l"(pair(v[2 * i], v[2 * i + 1])));
+    }
+    __device__ __forceinline__ void get(float (&v)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * i]), "=f"(v[2 * i + 1]) : "l"(s[i]));
+    }
+    __device__ __forceinline__ void set(const float (&v)[VEC]) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) s[i] = pair(v[2 * i], v[2 * i + 1]);
+    }
+};
+template <> struct Sums<1> {
+    float s;
+    static __device__ __forceinline__ uint64_t pair(float a, float b) { return Sums<2>::pair(a, b); }
+    __device__ __forceinline__ void zero() { s = 0.f; }
+    __device__ __forceinline__ void add(uint64_t ff, const float (&v)[1]) { s = fmaf(__uint_as_float(uint32_t(ff)), v[0], s); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = s; }
+    __device__ __forceinline__ void set(const float (&v)[1]) { s = v[0]; }
 };
 
 }  // namespace
