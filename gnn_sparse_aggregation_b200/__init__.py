@@ -29,7 +29,6 @@ A differential attention layer around the same graphs:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -497,16 +496,45 @@ def ag_attn_backward(g: Graph, Q, K, V, scale: float, alpha, dY, dQ=None, dK=Non
     return tuple(outs)
 
 
-@contextlib.contextmanager
-def _allocating_on(device: torch.device, stream):
-    """Tensors made inside belong to the stream that the call runs on, so that
-    their memory is not handed out again while the call's work is pending."""
-    if stream is None:
-        yield
-        return
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
-        yield
+class _At:
+    """Where a call runs: the stream's handle, and the allocations that belong
+    to that stream, so that their memory is not handed out again while the
+    call's work is pending."""
+
+    __slots__ = ("handle", "stream")
+
+    def __init__(self, device: torch.device, stream):
+        if stream is None:
+            self.stream = None
+            self.handle = _current_raw_stream(device.index)
+        else:
+            self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            self.stream = torch.cuda.ExternalStream(self.handle, device=device)
+
+    def like(self, of: torch.Tensor) -> torch.Tensor:
+        if self.stream is None:
+            return torch.empty_like(of)
+        with torch.cuda.stream(self.stream):
+            return torch.empty_like(of)
+
+    def empty(self, shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _current_raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without the Stream object around it, where torch has it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream)
+
+
+def _addr(t):
+    """The address argument of a tensor (None: absent, or nothing in it)."""
+    return None if t is None else t.data_ptr() or None
 
 
 def _u64(name: str, v: int) -> int:
@@ -516,21 +544,24 @@ def _u64(name: str, v: int) -> int:
     return v
 
 
-def _like(name: str, t, of: torch.Tensor) -> torch.Tensor:
-    """The output tensor `t`, checked against `of` (a new one where None)."""
-    if t is None:
-        return torch.empty_like(of)
+def _match(name: str, t, of: torch.Tensor) -> torch.Tensor:
+    """`t`, checked to be a CUDA tensor of the shape and dtype of `of`."""
     _need_cuda(name, t)
     if t.shape != of.shape or t.dtype != of.dtype:
         raise AggraphError(2, f"{name} must have shape {tuple(of.shape)} and dtype {of.dtype}")
     return t
 
 
+def _like(name: str, t, of: torch.Tensor, at: _At) -> torch.Tensor:
+    """The output tensor `t`, checked against `of` (a new one where None)."""
+    return at.like(of) if t is None else _match(name, t, of)
+
+
 def _vector(name: str, t, n: int) -> torch.Tensor:
     _need_cuda(name, t)
     if t.dtype != torch.float32:
         raise AggraphError(3, f"{name} must be float32")
-    if tuple(t.shape) != (n,):
+    if t.dim() != 1 or t.shape[0] != n:
         raise AggraphError(2, f"{name} must be [{n}], got {tuple(t.shape)}")
     return t
 
@@ -540,10 +571,10 @@ def ag_dropout(X: torch.Tensor, p: float, seed: int, offset: int = 0, out=None, 
     Philox4x32-10 block (i / 4, offset) under key `seed`.  The gradient is the same call on dY."""
     _need_cuda("X", X)
     code = _dtype_code(X)
-    with _allocating_on(X.device, stream):
-        out = _like("out", out, X)
-    _check(lib.ag_dropout(_ptr(X), _ptr(out), X.numel(), float(p), _u64("seed", seed), _u64("offset", offset), code,
-                          _stream(X.device, stream)))
+    at = _At(X.device, stream)
+    out = _like("out", out, X, at)
+    _check(lib.ag_dropout(_addr(X), _addr(out), X.numel(), float(p), _u64("seed", seed), _u64("offset", offset), code,
+                          at.handle))
     return out
 
 
@@ -558,7 +589,7 @@ def ag_rotary_freqs(rot: int, base: float = 10000.0, scaling: str = "none", fact
     inv_freq = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
     out = ctypes.c_double()
     _check(lib.ag_rotary_freqs(int(rot), float(base), _SCALINGS[scaling], float(factor), float(original),
-                               float(beta_fast), float(beta_slow), _ptr(inv_freq), ctypes.byref(out)))
+                               float(beta_fast), float(beta_slow), _addr(inv_freq), ctypes.byref(out)))
     return inv_freq, out.value
 
 
@@ -571,104 +602,107 @@ def ag_rotary(Q: torch.Tensor, K, pos: torch.Tensor, inv_freq: torch.Tensor, hea
         raise AggraphError(2, f"Q must be [N, H], got {tuple(Q.shape)}")
     code = _dtype_code(Q)
     N, H = Q.shape
-    for name, t, dtype, n in (("pos", pos, torch.int64, N), ("inv_freq", inv_freq, torch.float64, None)):
-        _need_cuda(name, t)
-        if t.dtype != dtype:
-            raise AggraphError(3, f"{name} must be {dtype}")
-        if t.dim() != 1 or (n is not None and t.shape[0] != n):
-            raise AggraphError(2, f"{name} must be one-dimensional{'' if n is None else f' of length {n}'}")
+    _need_cuda("pos", pos)
+    _need_cuda("inv_freq", inv_freq)
+    if pos.dtype != torch.int64 or inv_freq.dtype != torch.float64:
+        raise AggraphError(3, "pos must be int64 and inv_freq float64")
+    if pos.dim() != 1 or pos.shape[0] != N or inv_freq.dim() != 1:
+        raise AggraphError(2, f"pos must be [{N}] and inv_freq one-dimensional")
     if K is not None:
-        _like("K", K, Q)
+        _match("K", K, Q)
     elif Ko is not None:
         raise AggraphError(1, "Ko without K")
-    with _allocating_on(Q.device, stream):
-        Qo = _like("Qo", Qo, Q)
-        Ko = None if K is None else _like("Ko", Ko, K)
-    _check(lib.ag_rotary(_ptr(Q), _ptr(K), _ptr(pos), _ptr(inv_freq), _ptr(Qo), _ptr(Ko), N, H, int(heads),
+    at = _At(Q.device, stream)
+    Qo = _like("Qo", Qo, Q, at)
+    Ko = None if K is None else _like("Ko", Ko, K, at)
+    _check(lib.ag_rotary(_addr(Q), _addr(K), _addr(pos), _addr(inv_freq), _addr(Qo), _addr(Ko), N, H, int(heads),
                          2 * inv_freq.shape[0], int(bool(interleaved)), float(factor), int(bool(inverse)), code,
-                         _stream(Q.device, stream)))
+                         at.handle))
     return Qo, Ko
+
+
+def _diff_feats(g: Graph, names, ts, lam: torch.Tensor):
+    """(dtype code, H, heads, scratch bytes) of a differential attention call's inputs."""
+    first = ts[0]
+    code = _check_feat(g, names[0], first)
+    for name, t in zip(names[1:], ts[1:]):
+        _match(name, t, first)
+    _need_cuda("lam", lam)
+    H, heads = first.shape[1], lam.numel()
+    _vector("lam", lam, heads)
+    n = lib.ag_diff_attn_scratch_bytes(g.handle, H, heads)
+    if n == 0:
+        raise AggraphError(2, f"H = {H} is not 2 * heads * d with heads = {heads} in [1, 256] and d in [1, 256]")
+    return code, H, heads, n
+
+
+def _check_lse(g: Graph, lse: torch.Tensor, heads: int) -> torch.Tensor:
+    _need_cuda("lse", lse)
+    if lse.dtype != torch.float32:
+        raise AggraphError(3, "lse must be float32")
+    if tuple(lse.shape) != (g.N, heads, 2):
+        raise AggraphError(2, f"lse must be [{g.N}, {heads}, 2], got {tuple(lse.shape)}")
+    return lse
 
 
 def ag_diff_attn_fwd(g: Graph, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lam: torch.Tensor, scale: float,
                      p: float = 0.0, seed: int = 0, offset: int = 0, Y=None, lse=None, stream=None):
     """Differential edge-softmax attention of len(lam) heads: (Y, lse) with
     Y = sum over edges of u (alpha_1 - lam alpha_2) V and lse [N, heads, 2]."""
-    code = _same_feats(g, ("Q", "K", "V"), (Q, K, V))
-    _need_cuda("lam", lam)
-    heads = _vector("lam", lam, lam.numel()).shape[0]
-    H = Q.shape[1]
-    n = int(lib.ag_diff_attn_scratch_bytes(g.handle, H, heads))
-    if n == 0:
-        raise AggraphError(2, f"H = {H} is not 2 * heads * d with heads = {heads} in [1, 256] and d in [1, 256]")
-    with _allocating_on(g.device, stream):
-        Y = _like("Y", Y, V)
-        if lse is None:
-            lse = torch.empty((g.N, heads, 2), dtype=torch.float32, device=g.device)
-        else:
-            _check_lse(g, lse, heads)
-        scr = torch.empty(n, dtype=torch.uint8, device=g.device)
-    _check(lib.ag_diff_attn_fwd(g.handle, _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), float(scale), float(p),
-                                _u64("seed", seed), _u64("offset", offset), _ptr(Y), _ptr(lse), H, heads, code,
-                                _ptr(scr), n, _stream(g.device, stream)))
+    code, H, heads, n = _diff_feats(g, ("Q", "K", "V"), (Q, K, V), lam)
+    at = _At(g.device, stream)
+    Y = _like("Y", Y, V, at)
+    lse = at.empty((g.N, heads, 2), torch.float32, g.device) if lse is None else _check_lse(g, lse, heads)
+    scr = at.empty(n, torch.uint8, g.device)
+    _check(lib.ag_diff_attn_fwd(g.handle, _addr(Q), _addr(K), _addr(V), _addr(lam), float(scale), float(p),
+                                _u64("seed", seed), _u64("offset", offset), _addr(Y), _addr(lse), H, heads, code,
+                                _addr(scr), n, at.handle))
     return Y, lse
-
-
-def _check_lse(g: Graph, lse: torch.Tensor, heads: int) -> None:
-    _need_cuda("lse", lse)
-    if lse.dtype != torch.float32:
-        raise AggraphError(3, "lse must be float32")
-    if tuple(lse.shape) != (g.N, heads, 2):
-        raise AggraphError(2, f"lse must be [{g.N}, {heads}, 2], got {tuple(lse.shape)}")
 
 
 def ag_diff_attn_backward(g: Graph, Q, K, V, lam, scale: float, lse, dY, p: float = 0.0, seed: int = 0,
                           offset: int = 0, dQ=None, dK=None, dV=None, dlam=None, stream=None):
     """Gradients (dQ, dK, dV, dlam) of ag_diff_attn_fwd for the upstream gradient dY (p, seed
     and offset as in the forward call, lse from it)."""
-    code = _same_feats(g, ("Q", "K", "V", "dY"), (Q, K, V, dY))
-    _need_cuda("lam", lam)
-    heads = _vector("lam", lam, lam.numel()).shape[0]
-    H = Q.shape[1]
-    n = int(lib.ag_diff_attn_scratch_bytes(g.handle, H, heads))
-    if n == 0:
-        raise AggraphError(2, f"H = {H} is not 2 * heads * d with heads = {heads} in [1, 256] and d in [1, 256]")
+    code, H, heads, n = _diff_feats(g, ("Q", "K", "V", "dY"), (Q, K, V, dY), lam)
     _check_lse(g, lse, heads)
-    with _allocating_on(g.device, stream):
-        dQ, dK, dV = _like("dQ", dQ, Q), _like("dK", dK, K), _like("dV", dV, V)
-        dlam = torch.empty_like(lam) if dlam is None else _vector("dlam", dlam, heads)
-        scr = torch.empty(n, dtype=torch.uint8, device=g.device)
-    _check(lib.ag_diff_attn_backward(g.handle, _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), float(scale), float(p),
-                                     _u64("seed", seed), _u64("offset", offset), _ptr(lse), _ptr(dY), _ptr(dQ),
-                                     _ptr(dK), _ptr(dV), _ptr(dlam), H, heads, code, _ptr(scr), n,
-                                     _stream(g.device, stream)))
+    at = _At(g.device, stream)
+    dQ, dK, dV = _like("dQ", dQ, Q, at), _like("dK", dK, K, at), _like("dV", dV, V, at)
+    dlam = at.like(lam) if dlam is None else _vector("dlam", dlam, heads)
+    scr = at.empty(n, torch.uint8, g.device)
+    _check(lib.ag_diff_attn_backward(g.handle, _addr(Q), _addr(K), _addr(V), _addr(lam), float(scale), float(p),
+                                     _u64("seed", seed), _u64("offset", offset), _addr(lse), _addr(dY), _addr(dQ),
+                                     _addr(dK), _addr(dV), _addr(dlam), H, heads, code, _addr(scr), n, at.handle))
     return dQ, dK, dV, dlam
 
 
 _NORMS = {"rms": 0, "layer": 1}
 _ACTS = {"sigmoid": 0, "silu": 1}
+_NORM_VECTORS = ("gamma1", "beta1", "scale", "gamma2", "beta2")
 
 
-def _resnorm_op(H, gamma1, beta1, scale, gamma2, beta2, eps, norm, act, p, seed, offset) -> ResNorm:
+def _resnorm_op(H, vectors, eps, norm, act, p, seed, offset) -> ResNorm:
     if norm not in _NORMS or act not in _ACTS:
         raise AggraphError(1, f"unknown norm {norm!r} or gate {act!r}; expected one of {tuple(_NORMS)}, {tuple(_ACTS)}")
-    ptrs = []
-    for name, t in (("gamma1", gamma1), ("beta1", beta1), ("scale", scale), ("gamma2", gamma2), ("beta2", beta2)):
-        ptrs.append(None if t is None else _vector(name, t, H).data_ptr())
+    ptrs = [None if t is None else _vector(name, t, H).data_ptr() for name, t in zip(_NORM_VECTORS, vectors)]
     return ResNorm(*ptrs, float(p), _u64("seed", seed), _u64("offset", offset), float(eps), _NORMS[norm], _ACTS[act])
 
 
-def _resnorm_rows(named):
+def _resnorm_rows(names, ts):
     """(first tensor, dtype code) of the [N, H] matrices that are given, all alike."""
-    given = [(name, t) for name, t in named if t is not None]
-    if not given:
+    first = None
+    for name, t in zip(names, ts):
+        if t is None:
+            continue
+        if first is not None:
+            _match(name, t, first)
+            continue
+        _need_cuda(name, t)
+        if t.dim() != 2:
+            raise AggraphError(2, f"{name} must be [N, H], got {tuple(t.shape)}")
+        first = t
+    if first is None:
         raise AggraphError(1, "no matrix given")
-    first = given[0][1]
-    _need_cuda(given[0][0], first)
-    if first.dim() != 2:
-        raise AggraphError(2, f"{given[0][0]} must be [N, H], got {tuple(first.shape)}")
-    for name, t in given[1:]:
-        _like(name, t, first)
     return first, _dtype_code(first)
 
 
@@ -677,17 +711,17 @@ def ag_resnorm_fwd(R, B, G=None, gamma1=None, beta1=None, scale=None, gamma2=Non
                    next_norm: bool = True, X=None, Z=None, stream=None):
     """(X, Z): X = R + scale * drop(act(G) * (norm(B) gamma1 + beta1)) and Z = norm(X) gamma2 + beta2.
     Without B, X is R itself and Z its norm; next_norm=False leaves Z out (None)."""
-    first, code = _resnorm_rows((("R", R), ("B", B), ("G", G)))
-    op = _resnorm_op(first.shape[1], gamma1, beta1, scale, gamma2, beta2, eps, norm, act, p, seed, offset)
+    first, code = _resnorm_rows(("R", "B", "G"), (R, B, G))
+    op = _resnorm_op(first.shape[1], (gamma1, beta1, scale, gamma2, beta2), eps, norm, act, p, seed, offset)
     if B is None and X is not None:
         raise AggraphError(1, "X without a block output (the sum is R)")
     if not next_norm and Z is not None:
         raise AggraphError(1, "Z without the next norm")
-    with _allocating_on(first.device, stream):
-        X = None if B is None else _like("X", X, first)
-        Z = _like("Z", Z, first) if next_norm else None
-    _check(lib.ag_resnorm_fwd(ctypes.byref(op), _ptr(R), _ptr(B), _ptr(G), _ptr(X), _ptr(Z), first.shape[0],
-                              first.shape[1], code, _stream(first.device, stream)))
+    at = _At(first.device, stream)
+    X = None if B is None else _like("X", X, first, at)
+    Z = _like("Z", Z, first, at) if next_norm else None
+    _check(lib.ag_resnorm_fwd(ctypes.byref(op), _addr(R), _addr(B), _addr(G), _addr(X), _addr(Z), first.shape[0],
+                              first.shape[1], code, at.handle))
     return (R if B is None else X), Z
 
 
@@ -697,30 +731,31 @@ def ag_resnorm_backward(X, B, G, dX, dZ, gamma1=None, beta1=None, scale=None, ga
     """Gradients of ag_resnorm_fwd for dX and dZ (either may be None) from the stored sum X: a dict
     of "R" (the sum's gradient), "B", "G" and, for every vector that is given, "gamma1", "beta1",
     "scale", "gamma2", "beta2" (float32 [H])."""
-    first, code = _resnorm_rows((("X", X), ("B", B), ("G", G), ("dX", dX), ("dZ", dZ)))
+    first, code = _resnorm_rows(("X", "B", "G", "dX", "dZ"), (X, B, G, dX, dZ))
     N, H = first.shape
-    op = _resnorm_op(H, gamma1, beta1, scale, gamma2, beta2, eps, norm, act, p, seed, offset)
-    vectors = {"gamma1": gamma1, "beta1": beta1, "scale": scale, "gamma2": gamma2, "beta2": beta2}
-    if B is None and any(t is not None for t in (gamma1, beta1, scale)):
+    vectors = (gamma1, beta1, scale, gamma2, beta2)
+    op = _resnorm_op(H, vectors, eps, norm, act, p, seed, offset)
+    if B is None and not (gamma1 is None and beta1 is None and scale is None):
         raise AggraphError(1, "a vector of the block's norm without its output B")
-    if dZ is None and (gamma2 is not None or beta2 is not None):
+    if dZ is None and not (gamma2 is None and beta2 is None):
         raise AggraphError(1, "a vector of the next norm without dZ")
-    with _allocating_on(first.device, stream):
-        out = {"R": torch.empty_like(first)}
-        if B is not None:
-            out["B"] = torch.empty_like(first)
-        if G is not None:
-            out["G"] = torch.empty_like(first)
-        n = 0
-        if any(t is not None for t in vectors.values()):
-            n = int(lib.ag_resnorm_scratch_bytes(N, H))
-            for name, t in vectors.items():
-                if t is not None:
-                    out[name] = torch.empty_like(t)
-        scr = torch.empty(n, dtype=torch.uint8, device=first.device) if n else None
-    _check(lib.ag_resnorm_backward(ctypes.byref(op), _ptr(X), _ptr(B), _ptr(G), _ptr(dX), _ptr(dZ),
-                                   *[_ptr(out.get(k)) for k in ("R", "B", "G")], *[_ptr(out.get(k)) for k in vectors],
-                                   N, H, code, _ptr(scr), n, _stream(first.device, stream)))
+    at = _At(first.device, stream)
+    out = {"R": at.like(first)}
+    if B is not None:
+        out["B"] = at.like(first)
+    if G is not None:
+        out["G"] = at.like(first)
+    scr, n = None, 0
+    for name, t in zip(_NORM_VECTORS, vectors):
+        if t is not None:
+            out[name] = at.like(t)
+            n = 1
+    if n:
+        n = lib.ag_resnorm_scratch_bytes(N, H)
+        scr = at.empty(n, torch.uint8, first.device) if n else None
+    _check(lib.ag_resnorm_backward(ctypes.byref(op), _addr(X), _addr(B), _addr(G), _addr(dX), _addr(dZ),
+                                   _addr(out["R"]), *[_addr(out.get(k)) for k in ("B", "G") + _NORM_VECTORS],
+                                   N, H, code, _addr(scr), n, at.handle))
     return out
 
 

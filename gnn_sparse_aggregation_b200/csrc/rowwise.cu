@@ -18,25 +18,35 @@ constexpr int kSMs = 148;
 
 // ---------------------------------------------------------------------------- dropout
 
-// y_i = keep_i x_i / (1 - p).  A thread takes VEC (a multiple of 4)
-// consecutive elements per step: VEC / 4 Philox blocks.
+// y_i = keep_i x_i / (1 - p).  A thread takes kDropVecs vectors of VEC (a
+// multiple of 4) elements at a time, VEC / 4 Philox blocks each: the products
+// of one block run under the selections of another.
+constexpr int kDropVecs = 2;
+
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_dropout(const T *__restrict__ x, T *__restrict__ y, int64_t n, const Drop drop) {
     using F = Frag<T, VEC>;
     const int64_t vecs = n / VEC;
-    const int64_t stride = int64_t(gridDim.x) * blockDim.x;
+    const int64_t threads = int64_t(gridDim.x) * blockDim.x;
     const int64_t i0 = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    for (int64_t i = i0; i < vecs; i += stride) {
-        const typename F::raw r = F::load_stream(x + i * VEC);
-        float v[VEC];
-        F::unpack(r, v);
+    for (int64_t i = i0; i < vecs; i += kDropVecs * threads) {
+        typename F::raw r[kDropVecs];
 #pragma unroll
-        for (int q = 0; q < VEC / 4; ++q) {
-            const uint32_t k = keep4(uint64_t(i) * (VEC / 4) + q, drop);
+        for (int u = 0; u < kDropVecs; ++u)
+            r[u] = i + u * threads < vecs ? F::load_stream(x + (i + u * threads) * VEC) : F::zero();
+        uint32_t k[kDropVecs][VEC / 4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * q + j] = k >> j & 1u ? v[4 * q + j] * drop.scale : 0.f;
+        for (int q = 0; q < VEC / 4; ++q)
+#pragma unroll
+            for (int u = 0; u < kDropVecs; ++u) k[u][q] = keep4(uint64_t(i + u * threads) * (VEC / 4) + q, drop);
+#pragma unroll
+        for (int u = 0; u < kDropVecs; ++u) {
+            float v[VEC];
+            F::unpack(r[u], v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[j] = k[u][j / 4] >> (j & 3) & 1u ? v[j] * drop.scale : 0.f;
+            if (i + u * threads < vecs) F::store(y + (i + u * threads) * VEC, v);
         }
-        F::store(y + i * VEC, v);
     }
     // the last n % VEC elements
     const int64_t i = vecs * VEC + i0;
@@ -73,7 +83,7 @@ void launch_dropout(const void *X, void *Y, int64_t n, const Drop &drop, cudaStr
     const T *x = static_cast<const T *>(X);
     T *y = static_cast<T *>(Y);
     if ((uintptr_t(X) | uintptr_t(Y)) % (VEC * sizeof(T)) == 0)
-        k_dropout<T, VEC><<<grid_of(n / VEC + 1, 256, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
+        k_dropout<T, VEC><<<grid_of(n / VEC + 1, 256 * kDropVecs, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
     else
         k_dropout_scalar<T><<<grid_of((n + 3) / 4, 256, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
 }
@@ -112,50 +122,60 @@ __global__ void __launch_bounds__(256) k_rotary(const RotaryParams P) {
         turn[i] = make_float2(P.factor * c, P.sign * P.factor * s);
     }
     __syncthreads();
-    // units of a head: rotated (two vectors, or one with both halves of its pairs), then copied vectors
+    // units of a head: rotated (two vectors, or one with both halves of its
+    // pairs), then copied vectors.  A thread keeps its units and walks the rows.
     constexpr bool kPairInVec = !HALF && VEC > 1;
     const int rot_units = kPairInVec ? P.rot / VEC : pairs / VEC;
     const int head_units = rot_units + (P.D - P.rot) / VEC;
     const int row_units = head_units * P.heads;
-    const int total = rows * row_units * P.mats;
-    for (int i = threadIdx.x; i < total; i += blockDim.x) {
-        const int mat = i >= rows * row_units;
-        const int k = i - mat * rows * row_units;
-        const int r = k / row_units;
-        const int q = k - r * row_units;
+    const int lanes = row_units < int(blockDim.x) ? row_units : int(blockDim.x);  // threads of one row
+    const int row_step = int(blockDim.x) / lanes;
+    const int r0 = threadIdx.x / lanes;
+    if (r0 >= row_step) return;
+    for (int q = threadIdx.x % lanes; q < row_units; q += lanes) {
         const int head = q / head_units;
         const int u = q - head * head_units;
-        const int64_t base = (n0 + r) * P.H + int64_t(head) * P.D;
-        const T *x = static_cast<const T *>(mat ? P.in[1] : P.in[0]) + base;
-        T *y = static_cast<T *>(mat ? P.out[1] : P.out[0]) + base;
-        const float2 *cs = turn + r * pairs;
-        float a[VEC], b[VEC];
-        if (u >= rot_units) {
-            const int at = P.rot + (u - rot_units) * VEC;
-            F::unpack(F::load_stream(x + at), a);
-            F::store(y + at, a);
-        } else if (kPairInVec) {
-            F::unpack(F::load_stream(x + u * VEC), a);
+        const bool copied = u >= rot_units;
+        const int at = head * P.D + (copied ? P.rot + (u - rot_units) * VEC : (kPairInVec || HALF ? u * VEC : 2 * u));
+        const int other = HALF ? pairs : 1;     // from a pair's first to its second
+        const int pair0 = kPairInVec ? u * VEC / 2 : u * VEC;
+#pragma unroll 2
+        for (int r = r0; r < rows; r += row_step) {
+            const float2 *cs = turn + r * pairs + pair0;
+            float t[VEC][2];
+            if (!copied) {
 #pragma unroll
-            for (int v = 0; v + 1 < VEC; v += 2) {
-                const float2 t = cs[(u * VEC + v) / 2];
-                b[v] = a[v] * t.x - a[v + 1] * t.y;
-                b[v + 1] = a[v + 1] * t.x + a[v] * t.y;
+                for (int v = 0; v < (kPairInVec ? VEC / 2 : VEC); ++v) t[v][0] = cs[v].x, t[v][1] = cs[v].y;
             }
-            F::store(y + u * VEC, b);
-        } else {
-            const int at = HALF ? u * VEC : 2 * u, other = HALF ? at + pairs : at + 1;
-            F::unpack(F::load_stream(x + at), a);
-            F::unpack(F::load_stream(x + other), b);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float2 t = cs[HALF ? at + v : u];
-                const float p = a[v];
-                a[v] = p * t.x - b[v] * t.y;
-                b[v] = b[v] * t.x + p * t.y;
+            for (int mat = 0; mat < 2; ++mat) {
+                if (mat == P.mats) break;
+                const int64_t base = (n0 + r) * P.H + at;
+                const T *x = static_cast<const T *>(P.in[mat]) + base;
+                T *y = static_cast<T *>(P.out[mat]) + base;
+                float a[VEC], b[VEC];
+                F::unpack(F::load_stream(x), a);
+                if (copied) {
+                    F::store(y, a);
+                } else if (kPairInVec) {
+#pragma unroll
+                    for (int v = 0; v + 1 < VEC; v += 2) {
+                        b[v] = a[v] * t[v / 2][0] - a[v + 1] * t[v / 2][1];
+                        b[v + 1] = a[v + 1] * t[v / 2][0] + a[v] * t[v / 2][1];
+                    }
+                    F::store(y, b);
+                } else {
+                    F::unpack(F::load_stream(x + other), b);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        const float p = a[v];
+                        a[v] = p * t[v][0] - b[v] * t[v][1];
+                        b[v] = b[v] * t[v][0] + p * t[v][1];
+                    }
+                    F::store(y, a);
+                    F::store(y + other, b);
+                }
             }
-            F::store(y + at, a);
-            F::store(y + other, b);
         }
     }
 }
@@ -231,100 +251,157 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2 *red) {
     return v;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+// 1 / (1 + exp(-x)): off by at most (|x| + 4) 2^-24, relative
+__device__ __forceinline__ float sigmoid(float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    return __fdividef(1.f, 1.f + e);
+}
 
-template <int VEC, int NV>
-__device__ __forceinline__ float vec_of(const float *p, int c, int v, float none) {
-    return p ? __ldg(p + c + v) : none;
+// VEC values of a vector from column c on, or `none` where there is no vector
+template <int VEC>
+__device__ __forceinline__ void load_param(const float *p, int c, float none, float (&v)[VEC]) {
+    if (p) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += VEC < 4 ? 1 : 4) {
+            if constexpr (VEC < 4) {
+                v[i] = __ldg(p + c + i);
+            } else {
+                const float4 q = __ldg(reinterpret_cast<const float4 *>(p + c + i));
+                v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = none;
+    }
+}
+
+// Keep bits of VEC elements from i on (a multiple of VEC where VEC >= 4).
+template <int VEC>
+__device__ __forceinline__ uint32_t keep_vec(uint64_t i, const Drop &d) {
+    if constexpr (VEC == 1) return keep4(i >> 2, d) >> (i & 3) & 1u;
+    uint32_t k = 0;
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) k |= keep4((i >> 2) + q, d) << (4 * q);
+    return k;
+}
+
+constexpr int norm_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
+
+// x - mean(x) (layer), then 1 / sqrt(mean(x^2) + eps)
+template <int VEC, int NV, int TPR>
+__device__ __forceinline__ float normalise(float (&x)[NV][VEC], const bool (&ok)[NV], const NormParams &P, float2 *red) {
+    float2 s = make_float2(0.f, 0.f);
+    if (P.layer) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s.x += x[k][v];
+        const float mean = row_sum<TPR>(s, red).x * P.inv_h;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] - mean : 0.f;
+    }
+    s.x = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s.x = fmaf(x[k][v], x[k][v], s.x);
+    return rsqrtf(fmaf(row_sum<TPR>(s, red).x, P.inv_h, P.eps));
 }
 
 template <typename T, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_resnorm_fwd(const NormParams P) {
-    constexpr int THREADS = TPR < 256 ? 256 : TPR;
+__global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_fwd(const NormParams P) {
+    constexpr int THREADS = norm_threads(TPR);
     constexpr int RPB = THREADS / TPR;
+    constexpr bool AHEAD = NV * VEC <= 8 && TPR <= 256;  // the next row's loads, and the vectors, in registers
     using F = Frag<T, VEC>;
+    using raw = typename F::raw;
     __shared__ float2 red[THREADS / 32];
     const int l = threadIdx.x % TPR;
     bool ok[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) ok[k] = (l + k * TPR) * VEC < P.H;
-    for (int64_t n0 = int64_t(blockIdx.x) * RPB; n0 < P.N; n0 += int64_t(gridDim.x) * RPB) {
-        const int64_t n = n0 + threadIdx.x / TPR;
-        const bool row = n < P.N;
+    // scale / (1 - p) times gamma1 and beta1; gamma2, beta2
+    float g1[NV][VEC], b1[NV][VEC], g2[NV][VEC], b2[NV][VEC];
+    auto load_params = [&](int k) {
+        const int c = ok[k] ? (l + k * TPR) * VEC : 0;
+        float s[VEC];
+        load_param<VEC>(P.scale, c, 1.f, s);
+        load_param<VEC>(P.gamma1, c, 1.f, g1[k]);
+        load_param<VEC>(P.beta1, c, 0.f, b1[k]);
+        load_param<VEC>(P.gamma2, c, 1.f, g2[k]);
+        load_param<VEC>(P.beta2, c, 0.f, b2[k]);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] *= P.drop.scale, g1[k][v] *= s[v], b1[k][v] *= s[v];
+    };
+    raw nR[NV], nB[NV], nG[NV];
+    auto load_row = [&](int64_t n) {
         const int64_t at = n * P.H;
-        float x[NV][VEC], b[NV][VEC], g[NV][VEC];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (l + k * TPR) * VEC;
-            const bool in = row && ok[k];
-            F::unpack(in && P.R ? F::load_stream(static_cast<const T *>(P.R) + at + c) : F::zero(), x[k]);
-            F::unpack(in && P.B ? F::load_stream(static_cast<const T *>(P.B) + at + c) : F::zero(), b[k]);
-            F::unpack(in && P.G ? F::load_stream(static_cast<const T *>(P.G) + at + c) : F::zero(), g[k]);
+            const bool in = n < P.N && ok[k];
+            nR[k] = in && P.R ? F::load_stream(static_cast<const T *>(P.R) + at + c) : F::zero();
+            nB[k] = in && P.B ? F::load_stream(static_cast<const T *>(P.B) + at + c) : F::zero();
+            nG[k] = in && P.G ? F::load_stream(static_cast<const T *>(P.G) + at + c) : F::zero();
         }
+    };
+    const int64_t step = int64_t(gridDim.x) * RPB;
+    const int64_t first = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
+    if (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) load_params(k);
+        load_row(first);
+    }
+    for (int64_t n0 = int64_t(blockIdx.x) * RPB; n0 < P.N; n0 += step) {
+        const int64_t n = n0 + threadIdx.x / TPR;
+        const bool row = n < P.N;
+        const int64_t at = n * P.H;
+        if (!AHEAD) load_row(n);
+        float x[NV][VEC], b[NV][VEC], g[NV][VEC];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            F::unpack(nR[k], x[k]);
+            F::unpack(nB[k], b[k]);
+            F::unpack(nG[k], g[k]);
+        }
+        if (AHEAD) load_row(n + step);
         if (P.B) {
-            float2 s = make_float2(0.f, 0.f);
-            if (P.layer) {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) s.x += b[k][v];
-                const float mean = row_sum<TPR>(s, red).x * P.inv_h;
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) b[k][v] = ok[k] ? b[k][v] - mean : 0.f;
-            }
-            s = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) s.x = fmaf(b[k][v], b[k][v], s.x);
-            const float r = rsqrtf(fmaf(row_sum<TPR>(s, red).x, P.inv_h, P.eps));
+            const float r = normalise<VEC, NV, TPR>(b, ok, P, red);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = (l + k * TPR) * VEC;
-                if (!(row && ok[k])) continue;
-                const uint32_t kept = P.drop.on ? keep_bits(uint64_t(at + c), VEC, P.drop) : 0xffffffffu;
+                if (!AHEAD) load_params(k);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    float u = fmaf(b[k][v] * r, vec_of<VEC, NV>(P.gamma1, c, v, 1.f), vec_of<VEC, NV>(P.beta1, c, v, 0.f));
-                    if (P.G) {
-                        const float sg = sigmoid(g[k][v]);
-                        u *= P.silu ? g[k][v] * sg : sg;
+                for (int v = 0; v < VEC; ++v) b[k][v] = fmaf(b[k][v] * r, g1[k][v], b1[k][v]);
+                if (P.G) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        const float s = sigmoid(g[k][v]);
+                        b[k][v] *= P.silu ? g[k][v] * s : s;
                     }
-                    u = kept >> v & 1u ? u * P.drop.scale : 0.f;
-                    x[k][v] = fmaf(vec_of<VEC, NV>(P.scale, c, v, 1.f), u, x[k][v]);
                 }
-                F::store(static_cast<T *>(P.oX) + at + c, x[k]);
+                if (P.drop.on) {
+                    const uint32_t kept = keep_vec<VEC>(uint64_t(at + c), P.drop);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) b[k][v] = kept >> v & 1u ? b[k][v] : 0.f;
+                }
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] + b[k][v] : 0.f;
+                if (row && ok[k]) F::store(static_cast<T *>(P.oX) + at + c, x[k]);
             }
         }
         if (P.oZ) {
-            float2 s = make_float2(0.f, 0.f);
-            if (P.layer) {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) s.x += x[k][v];
-                const float mean = row_sum<TPR>(s, red).x * P.inv_h;
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] - mean : 0.f;
-            }
-            s = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) s.x = fmaf(x[k][v], x[k][v], s.x);
-            const float r = rsqrtf(fmaf(row_sum<TPR>(s, red).x, P.inv_h, P.eps));
+            const float r = normalise<VEC, NV, TPR>(x, ok, P, red);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = (l + k * TPR) * VEC;
-                if (!(row && ok[k])) continue;
+                if (!AHEAD) load_params(k);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    x[k][v] = fmaf(x[k][v] * r, vec_of<VEC, NV>(P.gamma2, c, v, 1.f), vec_of<VEC, NV>(P.beta2, c, v, 0.f));
-                F::store(static_cast<T *>(P.oZ) + at + c, x[k]);
+                for (int v = 0; v < VEC; ++v) x[k][v] = fmaf(x[k][v] * r, g2[k][v], b2[k][v]);
+                if (row && ok[k]) F::store(static_cast<T *>(P.oZ) + at + (l + k * TPR) * VEC, x[k]);
             }
         }
     }
@@ -341,8 +418,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_resnorm_fwd(const Nor
 // shared memory and writes one partial row, and k_resnorm_join adds the
 // blocks' in order.
 template <typename T, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_resnorm_bwd(const NormParams P) {
-    constexpr int THREADS = TPR < 256 ? 256 : TPR;
+__global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_bwd(const NormParams P) {
+    constexpr int THREADS = norm_threads(TPR);
     constexpr int RPB = THREADS / TPR;
     using F = Frag<T, VEC>;
     __shared__ float2 red[THREADS / 32];
@@ -374,38 +451,43 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_resnorm_bwd(const Nor
             F::unpack(in && P.dX ? F::load_stream(static_cast<const T *>(P.dX) + at + c) : F::zero(), dr[k]);
             rz[k] = in && P.dZ ? F::load_stream(static_cast<const T *>(P.dZ) + at + c) : F::zero();
             rg[k] = in && P.G ? F::load_stream(static_cast<const T *>(P.G) + at + c) : F::zero();
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) s.x += x[k][v], s.y += b[k][v];
         }
         if (P.layer) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s.x += x[k][v], s.y += b[k][v];
             s = row_sum<TPR>(s, red);
             const float mx = s.x * P.inv_h, mb = s.y * P.inv_h;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] - mx : 0.f, b[k][v] = ok[k] ? b[k][v] - mb : 0.f;
+            s = make_float2(0.f, 0.f);
         }
-        s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) s.x = fmaf(x[k][v], x[k][v], s.x), s.y = fmaf(b[k][v], b[k][v], s.y);
         s = row_sum<TPR>(s, red);
-        const float rx = rsqrtf(fmaf(s.x, P.inv_h, P.eps)), rb = rsqrtf(fmaf(s.y, P.inv_h, P.eps));
+        // (a row behind the last one adds nothing: its zeros times 0, not times 1 / sqrt(eps = 0))
+        const float rx = row ? rsqrtf(fmaf(s.x, P.inv_h, P.eps)) : 0.f;
+        const float rb = row ? rsqrtf(fmaf(s.y, P.inv_h, P.eps)) : 0.f;
         if (P.dZ) {
             float2 q = make_float2(0.f, 0.f);
             float y[NV][VEC];
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = (l + k * TPR) * VEC;
+                float gamma[VEC];
+                load_param<VEC>(P.gamma2, ok[k] ? (l + k * TPR) * VEC : 0, 1.f, gamma);
                 F::unpack(rz[k], y[k]);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    const float nx = x[k][v] * rx;
-                    sum[3][k][v] = fmaf(y[k][v], nx, sum[3][k][v]);
+                    x[k][v] *= rx;
+                    sum[3][k][v] = fmaf(y[k][v], x[k][v], sum[3][k][v]);
                     sum[4][k][v] += y[k][v];
-                    if (ok[k]) y[k][v] *= vec_of<VEC, NV>(P.gamma2, c, v, 1.f);
-                    q.x = fmaf(y[k][v], nx, q.x);
+                    y[k][v] *= gamma[v];
+                    q.x = fmaf(y[k][v], x[k][v], q.x);
                     q.y += y[k][v];
                 }
             }
@@ -414,55 +496,64 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_resnorm_bwd(const Nor
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) dr[k][v] = fmaf(rx, y[k][v] - c0 - x[k][v] * rx * c1, dr[k][v]);
+                for (int v = 0; v < VEC; ++v) dr[k][v] = fmaf(rx, fmaf(-x[k][v], c1, y[k][v] - c0), dr[k][v]);
         }
+        if (P.dR) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (row && ok[k] && P.dR) F::store(static_cast<T *>(P.dR) + at + (l + k * TPR) * VEC, dr[k]);
+            for (int k = 0; k < NV; ++k)
+                if (row && ok[k]) F::store(static_cast<T *>(P.dR) + at + (l + k * TPR) * VEC, dr[k]);
+        }
         if (P.B) {
             float2 q = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = (l + k * TPR) * VEC;
-                const bool in = row && ok[k];
-                const uint32_t kept = P.drop.on && in ? keep_bits(uint64_t(at + c), VEC, P.drop) : 0xffffffffu;
-                float g[VEC];
+                const int c = ok[k] ? (l + k * TPR) * VEC : 0;
+                float gamma[VEC], beta[VEC], sc[VEC], g[VEC];
+                load_param<VEC>(P.gamma1, c, 1.f, gamma);
+                load_param<VEC>(P.beta1, c, 0.f, beta);
+                load_param<VEC>(P.scale, c, 1.f, sc);
                 F::unpack(rg[k], g);
+                // (rows and columns outside hold dr = 0 or are not stored)
+                if (P.drop.on) {
+                    const uint32_t kept = keep_vec<VEC>(uint64_t(at + c), P.drop);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) dr[k][v] = kept >> v & 1u ? dr[k][v] * P.drop.scale : 0.f;
+                }
+                if (!ok[k]) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) dr[k][v] = 0.f;
+                }
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    const float gamma = ok[k] ? vec_of<VEC, NV>(P.gamma1, c, v, 1.f) : 0.f;
-                    const float beta = ok[k] ? vec_of<VEC, NV>(P.beta1, c, v, 0.f) : 0.f;
-                    const float sc = ok[k] ? vec_of<VEC, NV>(P.scale, c, v, 1.f) : 0.f;
                     const float nb = b[k][v] * rb;
                     b[k][v] = nb;
-                    const float u = fmaf(nb, gamma, beta);
+                    const float u = fmaf(nb, gamma[v], beta[v]);
                     float act = 1.f, slope = 0.f;
                     if (P.G) {
                         const float sg = sigmoid(g[v]);
-                        slope = sg * (1.f - sg);
                         act = sg;
+                        slope = fmaf(-sg, sg, sg);
                         if (P.silu) slope = fmaf(g[v], slope, sg), act = g[v] * sg;
                     }
-                    const float d = kept >> v & 1u ? dr[k][v] * P.drop.scale : 0.f;
+                    const float d = dr[k][v], ds = d * sc[v];
                     sum[2][k][v] = fmaf(d, act * u, sum[2][k][v]);
-                    const float ds = d * sc;
                     g[v] = ds * u * slope;
                     float du = ds * act;
                     sum[0][k][v] = fmaf(du, nb, sum[0][k][v]);
                     sum[1][k][v] += du;
-                    du *= gamma;
+                    du *= gamma[v];
                     dr[k][v] = du;
                     q.x = fmaf(du, nb, q.x);
                     q.y += du;
                 }
-                if (in && P.dG) F::store(static_cast<T *>(P.dG) + at + c, g);
+                if (row && ok[k] && P.dG) F::store(static_cast<T *>(P.dG) + at + c, g);
             }
             q = row_sum<TPR>(q, red);
             const float c1 = q.x * P.inv_h, c0 = P.layer ? q.y * P.inv_h : 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) dr[k][v] = rb * (dr[k][v] - c0 - b[k][v] * c1);
+                for (int v = 0; v < VEC; ++v) dr[k][v] = rb * fmaf(-b[k][v], c1, dr[k][v] - c0);
                 if (row && ok[k]) F::store(static_cast<T *>(P.dB) + at + (l + k * TPR) * VEC, dr[k]);
             }
         }
@@ -498,22 +589,26 @@ struct JoinParams {
     float *out[5];
     int blocks, H;
 };
-// Column sums of the blocks' partial rows: a warp-row of 32 columns per
-// block, its 8 warps each adding every 8th row, then the 8 in order.
-__global__ void __launch_bounds__(256) k_resnorm_join(const JoinParams P) {
-    __shared__ float red[8][32];
+// Column sums of the blocks' partial rows: a block takes 32 columns of one
+// vector, its 32 warps each add every 32nd row, then the 32 in order.
+__global__ void __launch_bounds__(1024) k_resnorm_join(const JoinParams P) {
+    __shared__ float red[32][33];
     float *out = P.out[blockIdx.y];
     if (!out) return;
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (c < P.H)
-        for (int b = w; b < P.blocks; b += 8) s += P.partial[(int64_t(b) * 5 + blockIdx.y) * P.H + c];
-    red[w][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (w == 0 && c < P.H) {
-        for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
-        out[c] = s;
+    if (c < P.H) {
+#pragma unroll 8
+        for (int b = w; b < P.blocks; b += 32) s += P.partial[(int64_t(b) * 5 + blockIdx.y) * P.H + c];
     }
+    red[w][lane] = s;
+    __syncthreads();
+    // warp w adds the 32 partial sums of column w by a fixed tree
+    s = red[lane][w];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (lane == 0 && blockIdx.x * 32 + w < P.H) out[blockIdx.x * 32 + w] = s;
 }
 
 constexpr int kMaxNormWidth = 8192;
@@ -525,44 +620,52 @@ int64_t norm_blocks(int64_t N, int64_t H) {
     return N < kSMs * per_sm ? N : kSMs * per_sm;
 }
 
-template <typename T, int VEC, int NV, int TPR>
-void launch_norm(const NormParams &P, bool back, int *blocks, cudaStream_t st) {
-    constexpr int THREADS = TPR < 256 ? 256 : TPR;
+template <typename T, int VEC, int NV, int TPR, bool BACK>
+void launch_norm(const NormParams &P, int *blocks, cudaStream_t st) {
+    constexpr int THREADS = norm_threads(TPR);
     constexpr int RPB = THREADS / TPR;
-    if (back) {
+    if constexpr (BACK) {
         *blocks = int(grid_of(P.N, RPB, norm_blocks(P.N, P.H)));
         k_resnorm_bwd<T, VEC, NV, TPR><<<*blocks, THREADS, 0, st>>>(P);
     } else {
         k_resnorm_fwd<T, VEC, NV, TPR><<<grid_of(P.N, RPB, kSMs * 16), THREADS, 0, st>>>(P);
     }
 }
-// Threads per row: the power of two that covers the row's vectors, up to 1024;
-// rows beyond that take more vectors per thread.
-template <typename T, int VEC>
-void dispatch_norm(const NormParams &P, bool back, int *blocks, cudaStream_t st) {
+// Threads per row: the power of two that covers the row's n vectors.  Up to
+// 64 vectors of four a row stays in a warp (two vectors a thread: no block
+// barrier in the row sums).
+template <typename T, int VEC, bool BACK>
+void dispatch_norm(const NormParams &P, int *blocks, cudaStream_t st) {
     const int n = (P.H + VEC - 1) / VEC;
-    if (n <= 4) launch_norm<T, VEC, 1, 4>(P, back, blocks, st);
-    else if (n <= 8) launch_norm<T, VEC, 1, 8>(P, back, blocks, st);
-    else if (n <= 16) launch_norm<T, VEC, 1, 16>(P, back, blocks, st);
-    else if (n <= 32) launch_norm<T, VEC, 1, 32>(P, back, blocks, st);
-    else if (n <= 64) launch_norm<T, VEC, 1, 64>(P, back, blocks, st);
-    else if (n <= 128) launch_norm<T, VEC, 1, 128>(P, back, blocks, st);
-    else if (n <= 256) launch_norm<T, VEC, 1, 256>(P, back, blocks, st);
-    else if (n <= 512) launch_norm<T, VEC, 1, 512>(P, back, blocks, st);
-    else if (n <= 1024) launch_norm<T, VEC, 1, 1024>(P, back, blocks, st);
-    else if constexpr (VEC == 4) launch_norm<T, VEC, 2, 1024>(P, back, blocks, st);
-    else if constexpr (VEC == 1) {
-        if (n <= 2048) launch_norm<T, VEC, 2, 1024>(P, back, blocks, st);
-        else launch_norm<T, VEC, 8, 1024>(P, back, blocks, st);
+    if constexpr (VEC == 1) {
+        if (n <= 32) launch_norm<T, VEC, 1, 32, BACK>(P, blocks, st);
+        else if (n <= 256) launch_norm<T, VEC, 8, 32, BACK>(P, blocks, st);
+        else if (n <= 2048) launch_norm<T, VEC, 8, 256, BACK>(P, blocks, st);
+        else launch_norm<T, VEC, 8, 1024, BACK>(P, blocks, st);
+    } else {
+        if (n <= 4) launch_norm<T, VEC, 1, 4, BACK>(P, blocks, st);
+        else if (n <= 8) launch_norm<T, VEC, 1, 8, BACK>(P, blocks, st);
+        else if (n <= 16) launch_norm<T, VEC, 1, 16, BACK>(P, blocks, st);
+        else if (n <= 32) launch_norm<T, VEC, 1, 32, BACK>(P, blocks, st);
+        else if (VEC == 4 && n <= 64) launch_norm<T, VEC, VEC == 4 ? 2 : 1, VEC == 4 ? 32 : 64, BACK>(P, blocks, st);
+        else if (VEC == 8 && n <= 64) launch_norm<T, VEC, 1, 64, BACK>(P, blocks, st);
+        else if (n <= 128) launch_norm<T, VEC, 1, 128, BACK>(P, blocks, st);
+        else if (n <= 256) launch_norm<T, VEC, 1, 256, BACK>(P, blocks, st);
+        else if (n <= 512) launch_norm<T, VEC, 1, 512, BACK>(P, blocks, st);
+        else if (n <= 1024) launch_norm<T, VEC, 1, 1024, BACK>(P, blocks, st);
+        else if constexpr (VEC == 4) launch_norm<T, VEC, 2, 1024, BACK>(P, blocks, st);
     }
 }
-template <typename T>
-void dispatch_norm(const NormParams &P, uintptr_t addresses, bool back, int *blocks, cudaStream_t st) {
-    constexpr int WIDE = sizeof(T) == 4 ? 4 : 8;
-    auto fits = [&](int vec) { return P.H % vec == 0 && addresses % (vec * sizeof(T)) == 0; };
-    if (fits(WIDE)) dispatch_norm<T, WIDE>(P, back, blocks, st);
-    else if (sizeof(T) == 2 && fits(4)) dispatch_norm<T, 4>(P, back, blocks, st);
-    else dispatch_norm<T, 1>(P, back, blocks, st);
+// The widest vector that divides the rows and every address.  Backward, four
+// features at most: the five column sums of eight take 40 registers.
+template <typename T, bool BACK>
+void dispatch_norm(const NormParams &P, uintptr_t addresses, uintptr_t vectors, int *blocks, cudaStream_t st) {
+    auto fits = [&](int vec) { return P.H % vec == 0 && addresses % (vec * sizeof(T)) == 0 && vectors % 16 == 0; };
+    if constexpr (sizeof(T) == 2 && !BACK) {
+        if (fits(8)) return dispatch_norm<T, 8, BACK>(P, blocks, st);
+    }
+    if (fits(4)) dispatch_norm<T, 4, BACK>(P, blocks, st);
+    else dispatch_norm<T, 1, BACK>(P, blocks, st);
 }
 
 // ---------------------------------------------------------------------------- checks
@@ -628,6 +731,10 @@ NormParams norm_params(const ag_resnorm *op, int64_t N, int64_t H) {
     P.inv_h = 1.f / float(H);
     P.drop = make_drop(op->p, op->seed, op->offset);
     return P;
+}
+
+uintptr_t vector_addresses(const NormParams &P) {
+    return uintptr_t(P.gamma1) | uintptr_t(P.beta1) | uintptr_t(P.scale) | uintptr_t(P.gamma2) | uintptr_t(P.beta2);
 }
 
 }  // namespace
@@ -760,8 +867,8 @@ int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, const voi
     P.oZ = Z;
     const uintptr_t at = uintptr_t(R) | uintptr_t(B) | uintptr_t(G) | uintptr_t(X) | uintptr_t(Z);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == AG_F32) dispatch_norm<float>(P, at, false, nullptr, st);
-    else dispatch_norm<bf16_t>(P, at, false, nullptr, st);
+    if (dtype == AG_F32) dispatch_norm<float, false>(P, at, vector_addresses(P), nullptr, st);
+    else dispatch_norm<bf16_t, false>(P, at, vector_addresses(P), nullptr, st);
     cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);
 }
@@ -819,8 +926,8 @@ int ag_resnorm_backward(const ag_resnorm *op, const void *X, const void *B, cons
         P.partial = any ? static_cast<float *>(scratch) : nullptr;
         uintptr_t at = uintptr_t(X) | uintptr_t(B) | uintptr_t(G) | uintptr_t(dX) | uintptr_t(dZ);
         at |= uintptr_t(dR) | uintptr_t(dB) | uintptr_t(dG);
-        if (dtype == AG_F32) dispatch_norm<float>(P, at, true, &blocks, st);
-        else dispatch_norm<bf16_t>(P, at, true, &blocks, st);
+        if (dtype == AG_F32) dispatch_norm<float, true>(P, at, vector_addresses(P), &blocks, st);
+        else dispatch_norm<bf16_t, true>(P, at, vector_addresses(P), &blocks, st);
     }
     if (any) {
         JoinParams J;
@@ -828,7 +935,7 @@ int ag_resnorm_backward(const ag_resnorm *op, const void *X, const void *B, cons
         for (int k = 0; k < 5; ++k) J.out[k] = sums[k];
         J.blocks = blocks;
         J.H = int(H);
-        k_resnorm_join<<<dim3(unsigned((H + 31) / 32), 5), 256, 0, st>>>(J);
+        k_resnorm_join<<<dim3(unsigned((H + 31) / 32), 5), 1024, 0, st>>>(J);
     }
     cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);

@@ -307,6 +307,17 @@ def test_resnorm_offset_rows_constant_rows_and_no_rows(agb):
     assert not d["gamma1"].any() and not d["gamma2"].any()
 
 
+def test_resnorm_eps_zero_and_rows_behind_the_last(agb):
+    # 7 rows fill no block: what stands in for further rows must not reach the column sums
+    N, H = 7, 32
+    m, v = _resnorm_case(N, H, torch.float32, 12)
+    d = agb.ag_resnorm_backward(m["X"], m["B"], m["G"], m["dX"], m["dZ"], eps=0.0, **v)
+    e = agb.ag_resnorm_backward(m["X"], m["B"], m["G"], m["dX"], m["dZ"], eps=1e-12, **v)
+    torch.cuda.synchronize()
+    for k in d:   # variances near 1: 1e-12 more changes a deviation by 5e-13, below a rounding
+        assert torch.isfinite(d[k]).all() and (d[k] - e[k]).abs().max() <= 64 * U * e[k].abs().max(), k
+
+
 def test_rowwise_streams_and_capture(agb):
     N, H = 700, 96
     m, v = _resnorm_case(N, H, torch.bfloat16, 3)
