@@ -78,9 +78,8 @@ template <typename T, int VEC> struct Frag {
         }
         return b.r;
     }
-    static __device__ __forceinline__ void store(T *p, const float (&v)[VEC]) {
-        __stcs(reinterpret_cast<raw *>(p), pack(v));
-    }
+    static __device__ __forceinline__ void store_raw(T *p, raw r) { __stcs(reinterpret_cast<raw *>(p), r); }
+    static __device__ __forceinline__ void store(T *p, const float (&v)[VEC]) { store_raw(p, pack(v)); }
     // c + the products of the fragments' elements, in order (bf16 products
     // are exact in fp32, so each term is rounded once)
     static __device__ __forceinline__ float dot(raw x, raw y, float c) {
@@ -137,6 +136,71 @@ template <> struct Sums<1> {
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = s; }
     __device__ __forceinline__ void set(const float (&v)[1]) { s = v[0]; }
 };
+
+// x = x * f + c element by element, two at a time where there are two
+template <int VEC>
+__device__ __forceinline__ void fma_all(float (&x)[VEC], const float (&f)[VEC], const float (&c)[VEC]) {
+    if constexpr (VEC == 1) {
+        x[0] = fmaf(x[0], f[0], c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            uint64_t v = Sums<2>::pair(x[i], x[i + 1]);
+            asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(Sums<2>::pair(f[i], f[i + 1])), "l"(Sums<2>::pair(c[i], c[i + 1])));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x[i]), "=f"(x[i + 1]) : "l"(v));
+        }
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void mul_all(float (&x)[VEC], float f) {
+    if constexpr (VEC == 1) {
+        x[0] *= f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            uint64_t v = Sums<2>::pair(x[i], x[i + 1]);
+            asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(Sums<2>::pair(f, f)));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x[i]), "=f"(x[i + 1]) : "l"(v));
+        }
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void add_all(float (&x)[VEC], const float (&y)[VEC]) {
+    if constexpr (VEC == 1) {
+        x[0] += y[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            uint64_t v = Sums<2>::pair(x[i], x[i + 1]);
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(Sums<2>::pair(y[i], y[i + 1])));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x[i]), "=f"(x[i + 1]) : "l"(v));
+        }
+    }
+}
+// sums of the elements and of their squares
+template <int VEC>
+__device__ __forceinline__ float sum_all(const float (&x)[VEC]) {
+    if constexpr (VEC == 1) return x[0];
+    uint64_t v = Sums<2>::pair(x[0], x[VEC > 1 ? 1 : 0]);
+#pragma unroll
+    for (int i = 2; i + 1 < VEC; i += 2) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(Sums<2>::pair(x[i], x[i + 1])));
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a + b;
+}
+template <int VEC>
+__device__ __forceinline__ float squares_all(const float (&x)[VEC]) {
+    if constexpr (VEC == 1) return x[0] * x[0];
+    uint64_t v = 0ull;
+#pragma unroll
+    for (int i = 0; i + 1 < VEC; i += 2) {
+        const uint64_t p = Sums<2>::pair(x[i], x[i + 1]);
+        asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(v) : "l"(p));
+    }
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a + b;
+}
 
 }  // namespace
 }  // namespace ag

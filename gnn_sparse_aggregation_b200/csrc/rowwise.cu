@@ -139,41 +139,57 @@ __global__ void __launch_bounds__(256) k_rotary(const RotaryParams P) {
         const int at = head * P.D + (copied ? P.rot + (u - rot_units) * VEC : (kPairInVec || HALF ? u * VEC : 2 * u));
         const int other = HALF ? pairs : 1;     // from a pair's first to its second
         const int pair0 = kPairInVec ? u * VEC / 2 : u * VEC;
-#pragma unroll 2
-        for (int r = r0; r < rows; r += row_step) {
-            const float2 *cs = turn + r * pairs + pair0;
-            float t[VEC][2];
-            if (!copied) {
+        // two rows of both matrices at a time: all their loads first
+        for (int r = r0; r < rows; r += 2 * row_step) {
+            typename F::raw ra[2][2], rb[2][2];
 #pragma unroll
-                for (int v = 0; v < (kPairInVec ? VEC / 2 : VEC); ++v) t[v][0] = cs[v].x, t[v][1] = cs[v].y;
+            for (int i = 0; i < 2; ++i) {
+                const int64_t base = (n0 + r + i * row_step) * P.H + at;
+                const bool in = r + i * row_step < rows;
+#pragma unroll
+                for (int mat = 0; mat < 2; ++mat) {
+                    const T *x = static_cast<const T *>(P.in[mat]) + base;
+                    const bool have = in && mat < P.mats;
+                    ra[i][mat] = have ? F::load_stream(x) : F::zero();
+                    if (!kPairInVec) rb[i][mat] = have && !copied ? F::load_stream(x + other) : F::zero();
+                }
             }
 #pragma unroll
-            for (int mat = 0; mat < 2; ++mat) {
-                if (mat == P.mats) break;
-                const int64_t base = (n0 + r) * P.H + at;
-                const T *x = static_cast<const T *>(P.in[mat]) + base;
-                T *y = static_cast<T *>(P.out[mat]) + base;
-                float a[VEC], b[VEC];
-                F::unpack(F::load_stream(x), a);
-                if (copied) {
-                    F::store(y, a);
-                } else if (kPairInVec) {
+            for (int i = 0; i < 2; ++i) {
+                const int ri = r + i * row_step;
+                if (ri >= rows) break;
+                const float2 *cs = turn + ri * pairs + (copied ? 0 : pair0);
+                float t[VEC][2];
 #pragma unroll
-                    for (int v = 0; v + 1 < VEC; v += 2) {
-                        b[v] = a[v] * t[v / 2][0] - a[v + 1] * t[v / 2][1];
-                        b[v + 1] = a[v + 1] * t[v / 2][0] + a[v] * t[v / 2][1];
-                    }
-                    F::store(y, b);
-                } else {
-                    F::unpack(F::load_stream(x + other), b);
+                for (int v = 0; v < (kPairInVec ? VEC / 2 : VEC); ++v) {
+                    const float2 f = copied ? make_float2(1.f, 0.f) : cs[v];
+                    t[v][0] = f.x, t[v][1] = f.y;
+                }
+                const int64_t base = (n0 + ri) * P.H + at;
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        const float p = a[v];
-                        a[v] = p * t[v][0] - b[v] * t[v][1];
-                        b[v] = b[v] * t[v][0] + p * t[v][1];
+                for (int mat = 0; mat < 2; ++mat) {
+                    if (mat == P.mats) break;
+                    T *y = static_cast<T *>(P.out[mat]) + base;
+                    float a[VEC], b[VEC];
+                    F::unpack(ra[i][mat], a);
+                    if constexpr (kPairInVec) {
+#pragma unroll
+                        for (int v = 0; v + 1 < VEC; v += 2) {
+                            b[v] = a[v] * t[v / 2][0] - a[v + 1] * t[v / 2][1];
+                            b[v + 1] = a[v + 1] * t[v / 2][0] + a[v] * t[v / 2][1];
+                        }
+                        F::store_raw(y, copied ? ra[i][mat] : F::pack(b));
+                    } else {
+                        F::unpack(rb[i][mat], b);
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            const float p = a[v];
+                            a[v] = p * t[v][0] - b[v] * t[v][1];
+                            b[v] = b[v] * t[v][0] + p * t[v][1];
+                        }
+                        F::store_raw(y, copied ? ra[i][mat] : F::pack(a));
+                        if (!copied) F::store(y + other, b);
                     }
-                    F::store(y, a);
-                    F::store(y + other, b);
                 }
             }
         }
@@ -289,26 +305,31 @@ __device__ __forceinline__ uint32_t keep_vec(uint64_t i, const Drop &d) {
 
 constexpr int norm_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
 
-// x - mean(x) (layer), then 1 / sqrt(mean(x^2) + eps)
+// x - mean(x) (layer), then 1 / sqrt(mean(x^2) + eps).  whole: every lane of
+// the row holds VEC * NV of its columns (else the others' stay 0).
 template <int VEC, int NV, int TPR>
-__device__ __forceinline__ float normalise(float (&x)[NV][VEC], const bool (&ok)[NV], const NormParams &P, float2 *red) {
+__device__ __forceinline__ float normalise(float (&x)[NV][VEC], const bool (&ok)[NV], bool whole, const NormParams &P,
+                                           float2 *red) {
     float2 s = make_float2(0.f, 0.f);
     if (P.layer) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) s.x += x[k][v];
+        for (int k = 0; k < NV; ++k) s.x += sum_all<VEC>(x[k]);
         const float mean = row_sum<TPR>(s, red).x * P.inv_h;
+        float minus[VEC];
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int v = 0; v < VEC; ++v) minus[v] = -mean;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] - mean : 0.f;
+        for (int k = 0; k < NV; ++k) {
+            add_all<VEC>(x[k], minus);
+            if (!whole && !ok[k]) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) x[k][v] = 0.f;
+            }
+        }
     }
     s.x = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) s.x = fmaf(x[k][v], x[k][v], s.x);
+    for (int k = 0; k < NV; ++k) s.x += squares_all<VEC>(x[k]);
     return rsqrtf(fmaf(row_sum<TPR>(s, red).x, P.inv_h, P.eps));
 }
 
@@ -324,6 +345,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_fwd(const NormPar
     bool ok[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) ok[k] = (l + k * TPR) * VEC < P.H;
+    const bool whole = P.H == TPR * NV * VEC;
     // scale / (1 - p) times gamma1 and beta1; gamma2, beta2
     float g1[NV][VEC], b1[NV][VEC], g2[NV][VEC], b2[NV][VEC];
     auto load_params = [&](int k) {
@@ -370,13 +392,13 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_fwd(const NormPar
         }
         if (AHEAD) load_row(n + step);
         if (P.B) {
-            const float r = normalise<VEC, NV, TPR>(b, ok, P, red);
+            const float r = normalise<VEC, NV, TPR>(b, ok, whole, P, red);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = (l + k * TPR) * VEC;
                 if (!AHEAD) load_params(k);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) b[k][v] = fmaf(b[k][v] * r, g1[k][v], b1[k][v]);
+                mul_all<VEC>(b[k], r);
+                fma_all<VEC>(b[k], g1[k], b1[k]);
                 if (P.G) {
 #pragma unroll
                     for (int v = 0; v < VEC; ++v) {
@@ -389,18 +411,21 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_fwd(const NormPar
 #pragma unroll
                     for (int v = 0; v < VEC; ++v) b[k][v] = kept >> v & 1u ? b[k][v] : 0.f;
                 }
+                if (!whole && !ok[k]) {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) x[k][v] = ok[k] ? x[k][v] + b[k][v] : 0.f;
+                    for (int v = 0; v < VEC; ++v) b[k][v] = 0.f;
+                }
+                add_all<VEC>(x[k], b[k]);
                 if (row && ok[k]) F::store(static_cast<T *>(P.oX) + at + c, x[k]);
             }
         }
         if (P.oZ) {
-            const float r = normalise<VEC, NV, TPR>(x, ok, P, red);
+            const float r = normalise<VEC, NV, TPR>(x, ok, whole, P, red);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 if (!AHEAD) load_params(k);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) x[k][v] = fmaf(x[k][v] * r, g2[k][v], b2[k][v]);
+                mul_all<VEC>(x[k], r);
+                fma_all<VEC>(x[k], g2[k], b2[k]);
                 if (row && ok[k]) F::store(static_cast<T *>(P.oZ) + at + (l + k * TPR) * VEC, x[k]);
             }
         }
