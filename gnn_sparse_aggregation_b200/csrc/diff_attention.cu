@@ -54,6 +54,7 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 2;            // warps per block
 constexpr int kMinBlocks = 8;        // per SM: at most 128 registers a thread
+constexpr int kResidentWarps = 148 * kMinBlocks * kWarps;
 constexpr int kZeroPerWarp = 32;     // rows without edges per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -78,6 +79,7 @@ struct DiffParams {
     int n_nz;
     unsigned tile_blocks;
     int T, H, heads, d, hb_log2;
+    int groups;                  // lane groups of a warp that walk a tile
     float c2;                    // scale * log2(e)
     float scale;
     Drop drop;
@@ -175,10 +177,12 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     // a tile per lane group; groups behind the last tile walk none (len 0)
     // (the last tiles first: nodes of few edges, whose tiles hold many rows and
     // take longest, tend to have the high ids)
-    const int64_t t0 = (int64_t(P.tile_blocks - 1 - blockIdx.x) * kWarps + (threadIdx.x >> 5)) * (32 / group_lanes);
+    const int64_t t0 = (int64_t(P.tile_blocks - 1 - blockIdx.x) * kWarps + (threadIdx.x >> 5)) * P.groups;
     if (t0 >= P.n_tiles) return;  // whole warps
     const int64_t t = t0 + lane / group_lanes;
-    const bool tile = t < P.n_tiles;
+    const bool tile = t < P.n_tiles && lane / group_lanes < P.groups;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) ok[k] = ok[k] && tile;
     const int64_t p0 = tile ? t * P.T : 0;
     const int len = tile ? int(P.E - p0 < P.T ? P.E - p0 : P.T) : 0;
     const int steps = int(P.E - t0 * P.T < P.T ? P.E - t0 * P.T : P.T);  // the first group's: the longest
@@ -244,8 +248,9 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     }
     const int32_t *const col = P.col + p0;
     const int last_unit = len > 0 ? (len - 1) & ~(U - 1) : 0;
-    // every group's tile is whole, with three units of positions behind it
-    const bool inner = __all_sync(kAll, tile && p0 + P.T + 3 * U <= P.E);
+    // every group's tile is whole, with three units of positions behind it (groups
+    // without a tile read the first one's ids and fetch nothing)
+    const bool inner = __all_sync(kAll, p0 + P.T + 3 * U <= P.E);
     struct Ids {
         int id[U];
     };
@@ -531,15 +536,15 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
         }
     }
     if (RING) cp_async_wait<0>();
-    if (row_begin < len) write_slot(before ? 2 * t : 2 * t + 1);  // the row open at the tile's end
+    if (tile && row_begin < len) write_slot(before ? 2 * t : 2 * t + 1);  // the row open at the tile's end
 }
 
 // Rows cut by tile boundaries: the partials of slot 2 first + 1 and of the
 // slots 2t of tiles first + 1 .. last.  A row cut into many tiles (those are
 // listed first) takes a block: a warp per (head, map) reduces its statistics
 // over the slots, then stripes of threads add every stripes-th slot's columns
-// and the stripes are added in order.  Every other row takes a warp, which
-// adds the slots in order.  All orders are fixed by the graph and the sizes.
+// and the stripes are added in order.  Every other row takes the lanes of its
+// columns, which add the slots in order.  All orders are fixed by the graph and the sizes.
 constexpr int kFixThreads = 512;
 
 struct FixParams {
@@ -551,7 +556,7 @@ struct FixParams {
     float *lse_out;
     float2 *stat;
     void *out_a, *out_b;
-    int H, heads, d;
+    int H, heads, d, lanes_log2;
     float scale, drop_scale;
 };
 
@@ -590,27 +595,25 @@ __device__ __forceinline__ void fix_columns(const FixParams &P, const Span &S, i
     }
 }
 
-// Statistics at index q of a slot: kFwd (M, L), kDQ (C, D' rebased to C), of
-// all slots (lanes = 1) or of one lane's share of a warp's.
-template <int MODE, bool WARP>
+// Statistics at index q of the slots, by a warp: kFwd (M, L), kDQ (C, D'
+// rebased to C).
+template <int MODE>
 __device__ __forceinline__ float2 fix_stats(const FixParams &P, const Span &S, int q) {
-    const int lane = WARP ? threadIdx.x & 31 : 0, step = WARP ? 32 : 1;
+    const int lane = threadIdx.x & 31;
     const int h2 = 2 * P.heads;
     if (MODE == kFwd) {
         float M = -3.402823466e38f;
-        for (int i = lane; i < S.n; i += step) M = fmaxf(M, S[i][q]);
-        if (WARP) {
+        for (int i = lane; i < S.n; i += 32) M = fmaxf(M, S[i][q]);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-        }
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
         float L = 0.f;
-        for (int i = lane; i < S.n; i += step) L = fmaf(S[i][q + h2], ex2(S[i][q] - M), L);
-        return make_float2(M, WARP ? group_sum<32>(L) : L);
+        for (int i = lane; i < S.n; i += 32) L = fmaf(S[i][q + h2], ex2(S[i][q] - M), L);
+        return make_float2(M, group_sum<32>(L));
     }
     const float C = S[0][q];
     float D = 0.f;
-    for (int i = lane; i < S.n; i += step) D += fmaf(S[i][q] - C, S[i][q + h2], S[i][q + 2 * h2]);
-    return make_float2(C, WARP ? group_sum<32>(D) : D);
+    for (int i = lane; i < S.n; i += 32) D += fmaf(S[i][q] - C, S[i][q + h2], S[i][q + 2 * h2]);
+    return make_float2(C, group_sum<32>(D));
 }
 
 template <typename T, int MODE, int CV>
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(kFixThreads) k_diff_fixup(const FixParams P) {
         const Span S(P, sp);
         if (MODE != kDKV) {
             for (int j = warp; j < 2 * P.heads; j += kFixThreads / 32) {
-                const float2 s = fix_stats<MODE, true>(P, S, q_at + j);
+                const float2 s = fix_stats<MODE>(P, S, q_at + j);
                 if (lane == 0) stats[j] = s;
             }
             __syncthreads();
@@ -677,27 +680,53 @@ __global__ void __launch_bounds__(kFixThreads) k_diff_fixup(const FixParams P) {
         }
         return;
     }
-    const int64_t s = P.n_long + (int64_t(blockIdx.x) - P.n_long) * (kFixThreads / 32) + warp;
+    // a group of lanes per row, in one pass over its slots: statistics and columns together
+    const int lanes = 1 << P.lanes_log2;
+    const int64_t s = P.n_long + (((int64_t(blockIdx.x) - P.n_long) * kFixThreads + threadIdx.x) >> P.lanes_log2);
     if (s >= P.n_span) return;
     const int4 sp = P.spans[s];
     const Span S(P, sp);
-    for (int c = lane * CV; c < P.H; c += 32 * CV) {
+    for (int c = (threadIdx.x & (lanes - 1)) * CV; c < P.H; c += lanes * CV) {
         const int head = c / (2 * P.d), map = c / P.d & 1;
-        const int q = q_at + 2 * head;
-        float2 s1 = make_float2(0.f, 1.f), s2 = s1;
-        if (MODE == kFwd) s1 = fix_stats<MODE, false>(P, S, q), s2 = fix_stats<MODE, false>(P, S, q + 1);
-        if (MODE == kDQ) s1 = fix_stats<MODE, false>(P, S, q + map);
+        const int q = q_at + 2 * head, h2 = 2 * P.heads;
+        float2 s1 = make_float2(-3.402823466e38f, 0.f), s2 = s1;
         float a[CV], b[CV];
-        fix_columns<MODE, CV>(P, S, 0, 1, c, q, map, make_float2(s1.x, s2.x), a, b);
+#pragma unroll
+        for (int v = 0; v < CV; ++v) a[v] = b[v] = 0.f;
+#pragma unroll 3
+        for (int i = 0; i < S.n; ++i) {
+            const float *p = S[i];
+            float u[CV], w[CV];
+            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c), u);
+            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c + P.H), w);
+            if (MODE == kFwd) {
+                const float m1 = fmaxf(s1.x, p[q]), m2 = fmaxf(s2.x, p[q + 1]);
+                const float f1 = ex2(s1.x - m1), g1 = ex2(p[q] - m1), f2 = ex2(s2.x - m2), g2 = ex2(p[q + 1] - m2);
+                s1 = make_float2(m1, fmaf(s1.y, f1, g1 * p[q + h2]));
+                s2 = make_float2(m2, fmaf(s2.y, f2, g2 * p[q + 1 + h2]));
+#pragma unroll
+                for (int v = 0; v < CV; ++v) a[v] = fmaf(a[v], f1, g1 * u[v]), b[v] = fmaf(b[v], f2, g2 * w[v]);
+            } else {
+                float shift = 0.f;
+                if (MODE == kDQ) {
+                    if (i == 0) s1 = make_float2(p[q + map], 0.f);
+                    shift = p[q + map] - s1.x;
+                    s1.y += fmaf(shift, p[q + map + h2], p[q + map + 2 * h2]);
+                }
+#pragma unroll
+                for (int v = 0; v < CV; ++v) a[v] += MODE == kDQ ? fmaf(shift, w[v], u[v]) : u[v], b[v] += w[v];
+            }
+        }
         fix_store<T, MODE, CV>(P, sp.x, c, head, map, s1, s2, a, b);
     }
 }
 
 // dlambda[h] = -sum over rows of D_2, in fp64: a thread adds rows of one head
-// (the rows' stride is fixed), a block its threads, and a second launch of one
-// block the blocks.
-constexpr int kLamBlocks = 296;
-constexpr int kLamThreads = 256;
+// (the rows' stride is fixed), a block its threads; with more than one block a
+// second launch of one adds the blocks (LAST).
+constexpr int kLamBlocks = 148;
+constexpr int kLamThreads = 1024;
+constexpr int kLamRows = 16;      // per thread at least, before another block takes part
 
 template <bool LAST>
 __global__ void __launch_bounds__(kLamThreads) k_diff_dlam(const float2 *__restrict__ stat, int64_t N, int heads,
@@ -706,7 +735,7 @@ __global__ void __launch_bounds__(kLamThreads) k_diff_dlam(const float2 *__restr
     const int per = kLamThreads / heads, h = threadIdx.x % heads, g = threadIdx.x / heads;
     double s = 0.0;
     if (g < per) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t r = int64_t(blockIdx.x) * per + g; r < N; r += int64_t(gridDim.x) * per)
             s += LAST ? partial[r * heads + h] : double(stat[(r * heads + h) * 2 + 1].y);
     }
@@ -719,7 +748,7 @@ __global__ void __launch_bounds__(kLamThreads) k_diff_dlam(const float2 *__restr
         __syncthreads();
     }
     if (threadIdx.x < heads) {
-        if (LAST) dlam[h] = float(-red[h]);
+        if (LAST || gridDim.x == 1) dlam[h] = float(-red[h]);
         else partial[int64_t(blockIdx.x) * heads + h] = red[h];
     }
 }
@@ -751,7 +780,11 @@ void launch_walk(DiffParams &P, cudaStream_t st) {
     int hb = 0;  // head slots: fill the warp, not beyond the heads
     while ((4 * DL << hb) <= 32 && (1 << hb) < P.heads) ++hb;
     P.hb_log2 = hb;
-    const int tiles = kWarps * (32 / (2 * DL << hb));  // per block
+    // as many tiles per warp as there are groups, but fewer while that leaves
+    // warps idle: a warp takes its groups' row ends one after another
+    P.groups = 32 / (2 * DL << hb);
+    while (P.groups > 1 && (P.n_tiles + P.groups - 1) / P.groups < kResidentWarps) P.groups >>= 1;
+    const int tiles = kWarps * P.groups;  // per block
     P.tile_blocks = unsigned((P.n_tiles + tiles - 1) / tiles);
     const int64_t zero = (P.n_zero + kWarps * kZeroPerWarp - 1) / (kWarps * kZeroPerWarp);
     const unsigned y = unsigned((P.heads + (1 << hb) - 1) >> hb);
@@ -818,9 +851,12 @@ void launch_fixup(const Direction &D, const DiffParams &P, int dtype, cudaStream
     F.d = P.d;
     F.scale = P.scale;
     F.drop_scale = P.drop.scale;
-    const unsigned grid = unsigned(F.n_long + (F.n_span - F.n_long + kFixThreads / 32 - 1) / (kFixThreads / 32));
     // four columns a thread where maps and rows divide so (slots are 16-byte aligned) and the outputs' addresses do
     const bool four = P.d % 4 == 0 && (uintptr_t(P.out_a) | uintptr_t(P.out_b)) % (dtype == AG_F32 ? 16 : 8) == 0;
+    F.lanes_log2 = 0;
+    while (F.lanes_log2 < 5 && (four ? 4 : 1) << F.lanes_log2 < F.H) ++F.lanes_log2;
+    const int rows = kFixThreads >> F.lanes_log2;
+    const unsigned grid = unsigned(F.n_long + (F.n_span - F.n_long + rows - 1) / rows);
     if (dtype == AG_F32) {
         if (four) k_diff_fixup<float, MODE, 4><<<grid, kFixThreads, 0, st>>>(F);
         else k_diff_fixup<float, MODE, 1><<<grid, kFixThreads, 0, st>>>(F);
@@ -964,11 +1000,11 @@ int ag_diff_attn_backward(const ag_graph *g, const void *Q, const void *K, const
     launch_fixup<kDQ>(g->dir[0], P, dtype, st);
     // dlambda from the rows' D
     double *part = reinterpret_cast<double *>(scr + L.dlam);
-    const int64_t per = 8 * (kLamThreads / heads);  // rows that fill a block
+    const int64_t per = kLamRows * (kLamThreads / heads);
     const int64_t want = (g->N + per - 1) / per;
     const int blocks = int(want < kLamBlocks ? want : kLamBlocks);
-    k_diff_dlam<false><<<blocks, kLamThreads, 0, st>>>(P.stat, g->N, int(heads), part, nullptr);
-    k_diff_dlam<true><<<1, kLamThreads, 0, st>>>(nullptr, blocks, int(heads), part, dlam);
+    k_diff_dlam<false><<<blocks, kLamThreads, 0, st>>>(P.stat, g->N, int(heads), part, dlam);
+    if (blocks > 1) k_diff_dlam<true><<<1, kLamThreads, 0, st>>>(nullptr, blocks, int(heads), part, dlam);
     // dK and dV over the source rows
     set_direction(P, g, 1);
     P.own_a = K;
