@@ -32,6 +32,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -126,10 +127,10 @@ def _bind(handle: ctypes.CDLL) -> ctypes.CDLL:
     handle.ag_diff_attn_scratch_bytes.restype = _SZ
     handle.ag_diff_attn_fwd.argtypes = [_P] * 5 + [_F, _D, _U64, _U64, _P, _P, _I64, _I64, _I, _P, _SZ, _P]
     handle.ag_diff_attn_backward.argtypes = [_P] * 5 + [_F, _D, _U64, _U64] + [_P] * 6 + [_I64, _I64, _I, _P, _SZ, _P]
-    handle.ag_resnorm_fwd.argtypes = [ctypes.POINTER(ResNorm)] + [_P] * 5 + [_I64, _I64, _I, _P]
+    handle.ag_resnorm_fwd.argtypes = [_P] + [_P] * 5 + [_I64, _I64, _I, _P]
     handle.ag_resnorm_scratch_bytes.argtypes = [_I64, _I64]
     handle.ag_resnorm_scratch_bytes.restype = _SZ
-    handle.ag_resnorm_backward.argtypes = [ctypes.POINTER(ResNorm)] + [_P] * 13 + [_I64, _I64, _I, _P, _SZ, _P]
+    handle.ag_resnorm_backward.argtypes = [_P] + [_P] * 13 + [_I64, _I64, _I, _P, _SZ, _P]
     handle.ag_graph_free.argtypes = [_P]
     handle.ag_graph_free.restype = None
     handle.ag_last_error.restype = ctypes.c_char_p
@@ -681,11 +682,14 @@ _ACTS = {"sigmoid": 0, "silu": 1}
 _NORM_VECTORS = ("gamma1", "beta1", "scale", "gamma2", "beta2")
 
 
-def _resnorm_op(H, vectors, eps, norm, act, p, seed, offset) -> ResNorm:
+_RESNORM = struct.Struct("5PdQQfii").pack  # the fields of ResNorm
+
+
+def _resnorm_op(H, vectors, eps, norm, act, p, seed, offset) -> bytes:
     if norm not in _NORMS or act not in _ACTS:
         raise AggraphError(1, f"unknown norm {norm!r} or gate {act!r}; expected one of {tuple(_NORMS)}, {tuple(_ACTS)}")
-    ptrs = [None if t is None else _vector(name, t, H).data_ptr() for name, t in zip(_NORM_VECTORS, vectors)]
-    return ResNorm(*ptrs, float(p), _u64("seed", seed), _u64("offset", offset), float(eps), _NORMS[norm], _ACTS[act])
+    ptrs = [0 if t is None else _vector(name, t, H).data_ptr() for name, t in zip(_NORM_VECTORS, vectors)]
+    return _RESNORM(*ptrs, float(p), _u64("seed", seed), _u64("offset", offset), float(eps), _NORMS[norm], _ACTS[act])
 
 
 def _resnorm_rows(names, ts):
@@ -720,7 +724,7 @@ def ag_resnorm_fwd(R, B, G=None, gamma1=None, beta1=None, scale=None, gamma2=Non
     at = _At(first.device, stream)
     X = None if B is None else _like("X", X, first, at)
     Z = _like("Z", Z, first, at) if next_norm else None
-    _check(lib.ag_resnorm_fwd(ctypes.byref(op), _addr(R), _addr(B), _addr(G), _addr(X), _addr(Z), first.shape[0],
+    _check(lib.ag_resnorm_fwd(op, _addr(R), _addr(B), _addr(G), _addr(X), _addr(Z), first.shape[0],
                               first.shape[1], code, at.handle))
     return (R if B is None else X), Z
 
@@ -753,7 +757,7 @@ def ag_resnorm_backward(X, B, G, dX, dZ, gamma1=None, beta1=None, scale=None, ga
     if n:
         n = lib.ag_resnorm_scratch_bytes(N, H)
         scr = at.empty(n, torch.uint8, first.device) if n else None
-    _check(lib.ag_resnorm_backward(ctypes.byref(op), _addr(X), _addr(B), _addr(G), _addr(dX), _addr(dZ),
+    _check(lib.ag_resnorm_backward(op, _addr(X), _addr(B), _addr(G), _addr(dX), _addr(dZ),
                                    _addr(out["R"]), *[_addr(out.get(k)) for k in ("B", "G") + _NORM_VECTORS],
                                    N, H, code, _addr(scr), n, at.handle))
     return out

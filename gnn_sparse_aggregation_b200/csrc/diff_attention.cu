@@ -77,7 +77,10 @@ struct DiffParams {
     int64_t n_zero, n_tiles;
     int64_t E;
     int n_nz;
-    unsigned tile_blocks;
+    unsigned tile_blocks, zero_blocks;
+    double *lam_partial;         // kDKV: sums of D_2 by block, [lam_blocks, heads]
+    int lam_blocks;
+    int64_t N;
     int T, H, heads, d, hb_log2;
     int groups;                  // lane groups of a warp that walk a tile
     float c2;                    // scale * log2(e)
@@ -108,6 +111,36 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     } else {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
     }
+}
+
+// dlambda[h] = -sum over rows of D_2, in fp64.  Blocks of the kDKV walk's
+// launch add rows (a thread rows of one head, at a fixed stride, then the
+// block its threads in a fixed tree), the last block of the kDKV fix-up's
+// launch adds their sums: no launch of its own, and under the walk's work.
+constexpr int kLamBlocks = 592;
+constexpr int kLamRows = 16;      // per thread at least, before another block takes part
+
+template <typename LOAD>
+__device__ __forceinline__ double lam_sum(double *red, int threads, int heads, int64_t n, int64_t block, int64_t blocks,
+                                          LOAD load) {
+    // threads beyond a multiple of the heads idle; more heads than threads go round (the caller loops)
+    const int per = threads / heads, g = threadIdx.x / heads, h = threadIdx.x % heads;
+    double s = 0.0;
+    if (g < per) {
+#pragma unroll 4
+        for (int64_t r = block * per + g; r < n; r += blocks * per) s += load(r, h);
+    }
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int k = per; k > 1;) {
+        const int half = (k + 1) / 2;
+        if (g < k - half) red[threadIdx.x] += red[threadIdx.x + half * heads];
+        k = half;
+        __syncthreads();
+    }
+    s = threadIdx.x < heads ? red[threadIdx.x] : 0.0;
+    __syncthreads();
+    return s;
 }
 
 // A running maximum is replaced only by a score beyond it by this much (in
@@ -153,6 +186,19 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     };
     const int stat_col = (live ? head : 0) * 2 + map;   // of [N, heads, 2]
 
+    if (MODE == kDKV && blockIdx.x >= P.tile_blocks + P.zero_blocks) {
+        if (blockIdx.y != 0) return;
+        __shared__ double sums[kWarps * 32];
+        const int block = int(blockIdx.x - P.tile_blocks - P.zero_blocks);
+        for (int h0 = 0; h0 < P.heads; h0 += kWarps * 32) {  // as many heads as threads at a time
+            const int heads = P.heads - h0 < kWarps * 32 ? P.heads - h0 : kWarps * 32;
+            const double s = lam_sum(sums, kWarps * 32, heads, P.N, block, P.lam_blocks, [&](int64_t r, int h) {
+                return double(P.stat[(r * P.heads + h0 + h) * 2 + 1].y);
+            });
+            if (threadIdx.x < heads) P.lam_partial[int64_t(block) * P.heads + h0 + threadIdx.x] = s;
+        }
+        return;
+    }
     if (blockIdx.x >= P.tile_blocks) {  // rows without edges
         const int64_t z0 = (int64_t(blockIdx.x - P.tile_blocks) * kWarps + (threadIdx.x >> 5)) * kZeroPerWarp;
         for (int i = lane / group_lanes; i < kZeroPerWarp && z0 + i < P.n_zero; i += 32 / group_lanes) {
@@ -540,11 +586,12 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
 }
 
 // Rows cut by tile boundaries: the partials of slot 2 first + 1 and of the
-// slots 2t of tiles first + 1 .. last.  A row cut into many tiles (those are
-// listed first) takes a block: a warp per (head, map) reduces its statistics
-// over the slots, then stripes of threads add every stripes-th slot's columns
-// and the stripes are added in order.  Every other row takes the lanes of its
-// columns, which add the slots in order.  All orders are fixed by the graph and the sizes.
+// slots 2t of tiles first + 1 .. last, in one pass (statistics and columns
+// together, as a softmax that runs over the slots).  A row cut into many tiles
+// (those are listed first) takes a block: stripes of threads take every
+// stripes-th slot, then the stripes are joined in order.  Every other row
+// takes the lanes of its columns, which take the slots in order.  All orders
+// are fixed by the graph and the sizes.
 constexpr int kFixThreads = 512;
 
 struct FixParams {
@@ -558,6 +605,9 @@ struct FixParams {
     void *out_a, *out_b;
     int H, heads, d, lanes_log2;
     float scale, drop_scale;
+    const double *lam_partial;   // kDKV: the last block adds up dlambda
+    float *dlam;
+    int lam_blocks;
 };
 
 struct Span {  // one cut row's slots, 0 .. n - 1
@@ -570,186 +620,138 @@ struct Span {  // one cut row's slots, 0 .. n - 1
     __device__ __forceinline__ const float *operator[](int i) const { return i == 0 ? first : rest + i * step; }
 };
 
-// CV columns from c on (of one map) over the slots i0, i0 + step, ...: a, b
-// are the two sums.  kFwd weights them by exp2(m - M) of their maps, kDQ adds
-// (c - C) B to A, where ref = (M1, M2) or (C, -).
+// A thread's sums over slots: CV columns of one map.  kFwd: s1, s2 the maps'
+// (maximum, sum), a, b their weighted sums; kDQ: s1 = (C, D'), a = A shifted
+// to C, b = B; kDKV: a, b.
 template <int MODE, int CV>
-__device__ __forceinline__ void fix_columns(const FixParams &P, const Span &S, int i0, int step, int c, int q0, int map,
-                                            float2 ref, float (&a)[CV], float (&b)[CV]) {
+struct FixSums {
+    float2 s1, s2;
+    float a[CV], b[CV];
+
+    __device__ __forceinline__ void start(float C) {
+        s1 = MODE == kDQ ? make_float2(C, 0.f) : make_float2(-3.402823466e38f, 0.f);
+        s2 = s1;
 #pragma unroll
-    for (int v = 0; v < CV; ++v) a[v] = b[v] = 0.f;
-#pragma unroll 4
-    for (int i = i0; i < S.n; i += step) {
-        const float *p = S[i] + c;
-        float u[CV], w[CV];
-        Frag<float, CV>::unpack(Frag<float, CV>::load(p), u);
-        Frag<float, CV>::unpack(Frag<float, CV>::load(p + P.H), w);
-        float f = 1.f, g = 1.f, shift = 0.f;
-        if (MODE == kFwd) f = ex2(S[i][q0] - ref.x), g = ex2(S[i][q0 + 1] - ref.y);
-        if (MODE == kDQ) shift = S[i][q0 + map] - ref.x;
+        for (int v = 0; v < CV; ++v) a[v] = b[v] = 0.f;
+    }
+    // the terms (t1, t2, u, w) of a slot or of another thread's sums; alpha: kDQ, the slot's sum of it
+    __device__ __forceinline__ void add(float2 t1, float2 t2, float alpha, const float (&u)[CV], const float (&w)[CV]) {
+        if (MODE == kFwd) {
+            const float m1 = fmaxf(s1.x, t1.x), m2 = fmaxf(s2.x, t2.x);
+            const float f1 = ex2(s1.x - m1), g1 = ex2(t1.x - m1), f2 = ex2(s2.x - m2), g2 = ex2(t2.x - m2);
+            s1 = make_float2(m1, fmaf(s1.y, f1, g1 * t1.y));
+            s2 = make_float2(m2, fmaf(s2.y, f2, g2 * t2.y));
 #pragma unroll
-        for (int v = 0; v < CV; ++v) {
-            a[v] = MODE == kDQ ? a[v] + fmaf(shift, w[v], u[v]) : fmaf(f, u[v], a[v]);
-            b[v] = fmaf(g, w[v], b[v]);
+            for (int v = 0; v < CV; ++v) a[v] = fmaf(a[v], f1, g1 * u[v]), b[v] = fmaf(b[v], f2, g2 * w[v]);
+        } else {
+            const float shift = MODE == kDQ ? t1.x - s1.x : 0.f;
+            if (MODE == kDQ) s1.y += fmaf(shift, alpha, t1.y);
+#pragma unroll
+            for (int v = 0; v < CV; ++v) a[v] += MODE == kDQ ? fmaf(shift, w[v], u[v]) : u[v], b[v] += w[v];
         }
     }
-}
-
-// Statistics at index q of the slots, by a warp: kFwd (M, L), kDQ (C, D'
-// rebased to C).
-template <int MODE>
-__device__ __forceinline__ float2 fix_stats(const FixParams &P, const Span &S, int q) {
-    const int lane = threadIdx.x & 31;
-    const int h2 = 2 * P.heads;
-    if (MODE == kFwd) {
-        float M = -3.402823466e38f;
-        for (int i = lane; i < S.n; i += 32) M = fmaxf(M, S[i][q]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-        float L = 0.f;
-        for (int i = lane; i < S.n; i += 32) L = fmaf(S[i][q + h2], ex2(S[i][q] - M), L);
-        return make_float2(M, group_sum<32>(L));
+    // slots i0, i0 + step, ...; q: where the head's statistics lie in a slot
+    __device__ __forceinline__ void add_slots(const FixParams &P, const Span &S, int i0, int step, int c, int q, int map) {
+        const int h2 = 2 * P.heads;
+#pragma unroll 4
+        for (int i = i0; i < S.n; i += step) {
+            const float *p = S[i];
+            float u[CV], w[CV];
+            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c), u);
+            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c + P.H), w);
+            if (MODE == kFwd) add(make_float2(p[q], p[q + h2]), make_float2(p[q + 1], p[q + 1 + h2]), 0.f, u, w);
+            else if (MODE == kDQ) add(make_float2(p[q + map], p[q + map + 2 * h2]), s2, p[q + map + h2], u, w);
+            else add(s1, s2, 0.f, u, w);
+        }
     }
-    const float C = S[0][q];
-    float D = 0.f;
-    for (int i = lane; i < S.n; i += 32) D += fmaf(S[i][q] - C, S[i][q + h2], S[i][q + 2 * h2]);
-    return make_float2(C, group_sum<32>(D));
-}
+};
 
 template <typename T, int MODE, int CV>
-__device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c, int head, int map, float2 s1, float2 s2,
-                                          float (&a)[CV], float (&b)[CV]) {
+__device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c, int head, int map,
+                                          FixSums<MODE, CV> &s) {
     const float lam = P.lam[head];
     float f = 1.f, g = 0.f;
-    if (MODE == kFwd) f = __fdividef(P.drop_scale, s1.y), g = -lam * __fdividef(P.drop_scale, s2.y);
-    if (MODE == kDQ) f = (map ? -lam : 1.f) * P.scale, g = -s1.y * f;  // s1: this map's (C, D')
+    if (MODE == kFwd) f = __fdividef(P.drop_scale, s.s1.y), g = -lam * __fdividef(P.drop_scale, s.s2.y);
+    if (MODE == kDQ) f = (map ? -lam : 1.f) * P.scale, g = -s.s1.y * f;
     T *out = static_cast<T *>(P.out_a) + row * P.H + c;
     if (MODE != kDKV) {
 #pragma unroll
-        for (int v = 0; v < CV; ++v) a[v] = fmaf(f, a[v], g * b[v]);
+        for (int v = 0; v < CV; ++v) s.a[v] = fmaf(f, s.a[v], g * s.b[v]);
     }
-    Frag<T, CV>::store(out, a);
-    if (MODE == kDKV) Frag<T, CV>::store(static_cast<T *>(P.out_b) + row * P.H + c, b);
+    Frag<T, CV>::store(out, s.a);
+    if (MODE == kDKV) Frag<T, CV>::store(static_cast<T *>(P.out_b) + row * P.H + c, s.b);
     if (MODE != kDKV && c % P.d == 0) {  // the map's statistics, once
         const int64_t k = (row * P.heads + head) * 2 + map;
-        const float2 s = MODE == kFwd && map ? s2 : s1;
-        if (MODE == kFwd) P.lse_out[k] = (s.x + log2f(s.y)) * kLn2;
-        if (MODE == kDQ) P.stat[k] = make_float2(P.lse[k] * kLog2e, s.x + s.y);
+        const float2 m = MODE == kFwd && map ? s.s2 : s.s1;
+        if (MODE == kFwd) P.lse_out[k] = (m.x + log2f(m.y)) * kLn2;
+        if (MODE == kDQ) P.stat[k] = make_float2(P.lse[k] * kLog2e, m.x + m.y);
     }
 }
 
 template <typename T, int MODE, int CV>
 __global__ void __launch_bounds__(kFixThreads) k_diff_fixup(const FixParams P) {
-    __shared__ float2 stats[MODE == kDKV ? 1 : 2 * kMaxHeads];  // long rows: per (head, map)
-    __shared__ float red[2 * CV][kFixThreads];
+    constexpr int kWords = 2 * CV + (MODE == kFwd ? 4 : (MODE == kDQ ? 1 : 0));
+    __shared__ float red[kWords][kFixThreads];
+    if (MODE == kDKV && P.lam_blocks > 0 && blockIdx.x == gridDim.x - 1) {
+        __shared__ double sums[kFixThreads];
+        const double s = lam_sum(sums, kFixThreads, P.heads, P.lam_blocks, 0, 1,
+                                 [&](int64_t b, int h) { return P.lam_partial[b * P.heads + h]; });
+        if (threadIdx.x < P.heads) P.dlam[threadIdx.x] = float(-s);
+        return;
+    }
     const int q_at = 2 * P.H;  // a slot's statistics
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    FixSums<MODE, CV> sum;
     if (blockIdx.x < P.n_long) {
         const int4 sp = P.spans[blockIdx.x];
         const Span S(P, sp);
-        if (MODE != kDKV) {
-            for (int j = warp; j < 2 * P.heads; j += kFixThreads / 32) {
-                const float2 s = fix_stats<MODE>(P, S, q_at + j);
-                if (lane == 0) stats[j] = s;
-            }
-            __syncthreads();
-        }
-        int cols = 32;
+        int cols = 1;
         while (cols * CV < P.H && cols < kFixThreads) cols <<= 1;
         const int stripes = kFixThreads / cols, stripe = threadIdx.x / cols, tc = threadIdx.x % cols;
         for (int c0 = 0; c0 < P.H; c0 += cols * CV) {
             const int c = c0 + tc * CV;
-            const int head = c / (2 * P.d), map = c / P.d & 1;
-            float a[CV], b[CV];
-            float2 s1 = make_float2(0.f, 1.f), s2 = s1;
+            const int head = c / (2 * P.d), map = c / P.d & 1, q = q_at + 2 * head;
             if (c < P.H) {
-                if (MODE == kFwd) s1 = stats[2 * head], s2 = stats[2 * head + 1];
-                if (MODE == kDQ) s1 = stats[2 * head + map];
-                fix_columns<MODE, CV>(P, S, stripe, stripes, c, q_at + 2 * head, map, make_float2(s1.x, s2.x), a, b);
+                sum.start(MODE == kDQ ? S[0][q + map] : 0.f);
+                sum.add_slots(P, S, stripe, stripes, c, q, map);
 #pragma unroll
-                for (int v = 0; v < CV; ++v) red[v][threadIdx.x] = a[v], red[CV + v][threadIdx.x] = b[v];
+                for (int v = 0; v < CV; ++v) red[v][threadIdx.x] = sum.a[v], red[CV + v][threadIdx.x] = sum.b[v];
+                if constexpr (MODE == kDQ) red[2 * CV][threadIdx.x] = sum.s1.y;
+                if constexpr (MODE == kFwd) {
+                    red[2 * CV][threadIdx.x] = sum.s1.x, red[2 * CV + 1][threadIdx.x] = sum.s1.y;
+                    red[2 * CV + 2][threadIdx.x] = sum.s2.x, red[2 * CV + 3][threadIdx.x] = sum.s2.y;
+                }
             }
             __syncthreads();
             if (stripe == 0 && c < P.H) {
-                for (int k = 1; k < stripes; ++k)
+                for (int k = 1; k < stripes; ++k) {
+                    const int i = k * cols + tc;
+                    float u[CV], w[CV];
 #pragma unroll
-                    for (int v = 0; v < CV; ++v) a[v] += red[v][k * cols + tc], b[v] += red[CV + v][k * cols + tc];
-                fix_store<T, MODE, CV>(P, sp.x, c, head, map, s1, s2, a, b);
+                    for (int v = 0; v < CV; ++v) u[v] = red[v][i], w[v] = red[CV + v][i];
+                    float2 t1 = sum.s1, t2 = sum.s2;
+                    if constexpr (MODE == kDQ) t1.y = red[2 * CV][i];  // the same C
+                    if constexpr (MODE == kFwd) {
+                        t1 = make_float2(red[2 * CV][i], red[2 * CV + 1][i]);
+                        t2 = make_float2(red[2 * CV + 2][i], red[2 * CV + 3][i]);
+                    }
+                    sum.add(t1, t2, 0.f, u, w);
+                }
+                fix_store<T, MODE, CV>(P, sp.x, c, head, map, sum);
             }
             __syncthreads();
         }
         return;
     }
-    // a group of lanes per row, in one pass over its slots: statistics and columns together
     const int lanes = 1 << P.lanes_log2;
     const int64_t s = P.n_long + (((int64_t(blockIdx.x) - P.n_long) * kFixThreads + threadIdx.x) >> P.lanes_log2);
     if (s >= P.n_span) return;
     const int4 sp = P.spans[s];
     const Span S(P, sp);
     for (int c = (threadIdx.x & (lanes - 1)) * CV; c < P.H; c += lanes * CV) {
-        const int head = c / (2 * P.d), map = c / P.d & 1;
-        const int q = q_at + 2 * head, h2 = 2 * P.heads;
-        float2 s1 = make_float2(-3.402823466e38f, 0.f), s2 = s1;
-        float a[CV], b[CV];
-#pragma unroll
-        for (int v = 0; v < CV; ++v) a[v] = b[v] = 0.f;
-#pragma unroll 3
-        for (int i = 0; i < S.n; ++i) {
-            const float *p = S[i];
-            float u[CV], w[CV];
-            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c), u);
-            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c + P.H), w);
-            if (MODE == kFwd) {
-                const float m1 = fmaxf(s1.x, p[q]), m2 = fmaxf(s2.x, p[q + 1]);
-                const float f1 = ex2(s1.x - m1), g1 = ex2(p[q] - m1), f2 = ex2(s2.x - m2), g2 = ex2(p[q + 1] - m2);
-                s1 = make_float2(m1, fmaf(s1.y, f1, g1 * p[q + h2]));
-                s2 = make_float2(m2, fmaf(s2.y, f2, g2 * p[q + 1 + h2]));
-#pragma unroll
-                for (int v = 0; v < CV; ++v) a[v] = fmaf(a[v], f1, g1 * u[v]), b[v] = fmaf(b[v], f2, g2 * w[v]);
-            } else {
-                float shift = 0.f;
-                if (MODE == kDQ) {
-                    if (i == 0) s1 = make_float2(p[q + map], 0.f);
-                    shift = p[q + map] - s1.x;
-                    s1.y += fmaf(shift, p[q + map + h2], p[q + map + 2 * h2]);
-                }
-#pragma unroll
-                for (int v = 0; v < CV; ++v) a[v] += MODE == kDQ ? fmaf(shift, w[v], u[v]) : u[v], b[v] += w[v];
-            }
-        }
-        fix_store<T, MODE, CV>(P, sp.x, c, head, map, s1, s2, a, b);
-    }
-}
-
-// dlambda[h] = -sum over rows of D_2, in fp64: a thread adds rows of one head
-// (the rows' stride is fixed), a block its threads; with more than one block a
-// second launch of one adds the blocks (LAST).
-constexpr int kLamBlocks = 148;
-constexpr int kLamThreads = 1024;
-constexpr int kLamRows = 16;      // per thread at least, before another block takes part
-
-template <bool LAST>
-__global__ void __launch_bounds__(kLamThreads) k_diff_dlam(const float2 *__restrict__ stat, int64_t N, int heads,
-                                                           double *__restrict__ partial, float *__restrict__ dlam) {
-    __shared__ double red[kLamThreads];
-    const int per = kLamThreads / heads, h = threadIdx.x % heads, g = threadIdx.x / heads;
-    double s = 0.0;
-    if (g < per) {
-#pragma unroll 8
-        for (int64_t r = int64_t(blockIdx.x) * per + g; r < N; r += int64_t(gridDim.x) * per)
-            s += LAST ? partial[r * heads + h] : double(stat[(r * heads + h) * 2 + 1].y);
-    }
-    red[threadIdx.x] = s;
-    __syncthreads();
-    for (int n = per; n > 1;) {
-        const int half = (n + 1) / 2;
-        if (g < n - half) red[threadIdx.x] += red[threadIdx.x + half * heads];
-        n = half;
-        __syncthreads();
-    }
-    if (threadIdx.x < heads) {
-        if (LAST || gridDim.x == 1) dlam[h] = float(-red[h]);
-        else partial[int64_t(blockIdx.x) * heads + h] = red[h];
+        const int head = c / (2 * P.d), map = c / P.d & 1, q = q_at + 2 * head;
+        sum.start(MODE == kDQ ? S[0][q + map] : 0.f);
+        sum.add_slots(P, S, 0, 1, c, q, map);
+        fix_store<T, MODE, CV>(P, sp.x, c, head, map, sum);
     }
 }
 
@@ -788,7 +790,8 @@ void launch_walk(DiffParams &P, cudaStream_t st) {
     P.tile_blocks = unsigned((P.n_tiles + tiles - 1) / tiles);
     const int64_t zero = (P.n_zero + kWarps * kZeroPerWarp - 1) / (kWarps * kZeroPerWarp);
     const unsigned y = unsigned((P.heads + (1 << hb) - 1) >> hb);
-    const dim3 grid(unsigned(P.tile_blocks + zero), y);
+    P.zero_blocks = unsigned(zero);
+    const dim3 grid(P.tile_blocks + P.zero_blocks + (MODE == kDKV ? P.lam_blocks : 0), y);
     if (grid.x == 0) return;
     if (P.drop.on) k_diff_walk<T, VEC, DL, NV, MODE, true><<<grid, kWarps * 32, 0, st>>>(P);
     else k_diff_walk<T, VEC, DL, NV, MODE, false><<<grid, kWarps * 32, 0, st>>>(P);
@@ -832,9 +835,9 @@ void launch_mode(DiffParams &P, int dtype, uintptr_t addresses, cudaStream_t st)
 }
 
 template <int MODE>
-void launch_fixup(const Direction &D, const DiffParams &P, int dtype, cudaStream_t st) {
-    if (D.n_span == 0) return;
-    FixParams F;
+void launch_fixup(const Direction &D, const DiffParams &P, int dtype, float *dlam, cudaStream_t st) {
+    if (D.n_span == 0 && MODE != kDKV) return;
+    FixParams F = {};
     F.spans = D.spans;
     F.n_long = D.n_span_long;
     F.n_span = D.n_span;
@@ -851,12 +854,15 @@ void launch_fixup(const Direction &D, const DiffParams &P, int dtype, cudaStream
     F.d = P.d;
     F.scale = P.scale;
     F.drop_scale = P.drop.scale;
+    F.lam_partial = P.lam_partial;
+    F.lam_blocks = MODE == kDKV ? P.lam_blocks : 0;
+    F.dlam = dlam;
     // four columns a thread where maps and rows divide so (slots are 16-byte aligned) and the outputs' addresses do
     const bool four = P.d % 4 == 0 && (uintptr_t(P.out_a) | uintptr_t(P.out_b)) % (dtype == AG_F32 ? 16 : 8) == 0;
     F.lanes_log2 = 0;
     while (F.lanes_log2 < 5 && (four ? 4 : 1) << F.lanes_log2 < F.H) ++F.lanes_log2;
     const int rows = kFixThreads >> F.lanes_log2;
-    const unsigned grid = unsigned(F.n_long + (F.n_span - F.n_long + rows - 1) / rows);
+    const unsigned grid = unsigned(F.n_long + (F.n_span - F.n_long + rows - 1) / rows) + (MODE == kDKV ? 1 : 0);
     if (dtype == AG_F32) {
         if (four) k_diff_fixup<float, MODE, 4><<<grid, kFixThreads, 0, st>>>(F);
         else k_diff_fixup<float, MODE, 1><<<grid, kFixThreads, 0, st>>>(F);
@@ -965,7 +971,7 @@ int ag_diff_attn_fwd(const ag_graph *g, const void *Q, const void *K, const void
     P.lse_out = lse;
     const uintptr_t at = uintptr_t(Q) | uintptr_t(K) | uintptr_t(V) | uintptr_t(Y);
     launch_mode<kFwd>(P, dtype, at, st);
-    launch_fixup<kFwd>(g->dir[0], P, dtype, st);
+    launch_fixup<kFwd>(g->dir[0], P, dtype, nullptr, st);
     cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);
 }
@@ -997,15 +1003,13 @@ int ag_diff_attn_backward(const ag_graph *g, const void *Q, const void *K, const
     P.out_a = dQ;
     const uintptr_t in = uintptr_t(Q) | uintptr_t(K) | uintptr_t(V) | uintptr_t(dY);
     launch_mode<kDQ>(P, dtype, in | uintptr_t(dQ), st);
-    launch_fixup<kDQ>(g->dir[0], P, dtype, st);
-    // dlambda from the rows' D
-    double *part = reinterpret_cast<double *>(scr + L.dlam);
-    const int64_t per = kLamRows * (kLamThreads / heads);
+    launch_fixup<kDQ>(g->dir[0], P, dtype, nullptr, st);
+    // dK and dV over the source rows, and dlambda from the rows' D
+    P.N = g->N;
+    P.lam_partial = reinterpret_cast<double *>(scr + L.dlam);
+    const int64_t per = kLamRows * (heads < kWarps * 32 ? kWarps * 32 / heads : 1);
     const int64_t want = (g->N + per - 1) / per;
-    const int blocks = int(want < kLamBlocks ? want : kLamBlocks);
-    k_diff_dlam<false><<<blocks, kLamThreads, 0, st>>>(P.stat, g->N, int(heads), part, dlam);
-    if (blocks > 1) k_diff_dlam<true><<<1, kLamThreads, 0, st>>>(nullptr, blocks, int(heads), part, dlam);
-    // dK and dV over the source rows
+    P.lam_blocks = int(want < kLamBlocks ? want : kLamBlocks);
     set_direction(P, g, 1);
     P.own_a = K;
     P.own_b = V;
@@ -1014,7 +1018,7 @@ int ag_diff_attn_backward(const ag_graph *g, const void *Q, const void *K, const
     P.out_a = dK;
     P.out_b = dV;
     launch_mode<kDKV>(P, dtype, in | uintptr_t(dK) | uintptr_t(dV), st);
-    launch_fixup<kDKV>(g->dir[1], P, dtype, st);
+    launch_fixup<kDKV>(g->dir[1], P, dtype, dlam, st);
     cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);
 }
