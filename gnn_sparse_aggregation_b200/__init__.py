@@ -518,11 +518,12 @@ class _At:
         with torch.cuda.stream(self.stream):
             return torch.empty_like(of)
 
-    def empty(self, shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    def floats(self, shape, of: torch.Tensor) -> torch.Tensor:
+        """A new float32 tensor on the device of `of` (float32 itself)."""
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
+            return of.new_empty(shape)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+            return of.new_empty(shape)
 
 
 def _current_raw_stream(index: int) -> int:
@@ -653,8 +654,8 @@ def ag_diff_attn_fwd(g: Graph, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor
     code, H, heads, n = _diff_feats(g, ("Q", "K", "V"), (Q, K, V), lam)
     at = _At(g.device, stream)
     Y = _like("Y", Y, V, at)
-    lse = at.empty((g.N, heads, 2), torch.float32, g.device) if lse is None else _check_lse(g, lse, heads)
-    scr = at.empty(n, torch.uint8, g.device)
+    lse = at.floats((g.N, heads, 2), lam) if lse is None else _check_lse(g, lse, heads)
+    scr = at.floats((n + 3) // 4, lam)
     _check(lib.ag_diff_attn_fwd(g.handle, _addr(Q), _addr(K), _addr(V), _addr(lam), float(scale), float(p),
                                 _u64("seed", seed), _u64("offset", offset), _addr(Y), _addr(lse), H, heads, code,
                                 _addr(scr), n, at.handle))
@@ -670,7 +671,7 @@ def ag_diff_attn_backward(g: Graph, Q, K, V, lam, scale: float, lse, dY, p: floa
     at = _At(g.device, stream)
     dQ, dK, dV = _like("dQ", dQ, Q, at), _like("dK", dK, K, at), _like("dV", dV, V, at)
     dlam = at.like(lam) if dlam is None else _vector("dlam", dlam, heads)
-    scr = at.empty(n, torch.uint8, g.device)
+    scr = at.floats((n + 3) // 4, lam)
     _check(lib.ag_diff_attn_backward(g.handle, _addr(Q), _addr(K), _addr(V), _addr(lam), float(scale), float(p),
                                      _u64("seed", seed), _u64("offset", offset), _addr(lse), _addr(dY), _addr(dQ),
                                      _addr(dK), _addr(dV), _addr(dlam), H, heads, code, _addr(scr), n, at.handle))
@@ -752,11 +753,10 @@ def ag_resnorm_backward(X, B, G, dX, dZ, gamma1=None, beta1=None, scale=None, ga
     scr, n = None, 0
     for name, t in zip(_NORM_VECTORS, vectors):
         if t is not None:
+            if scr is None:
+                n = lib.ag_resnorm_scratch_bytes(N, H)
+                scr = at.floats((n + 3) // 4, t)
             out[name] = at.like(t)
-            n = 1
-    if n:
-        n = lib.ag_resnorm_scratch_bytes(N, H)
-        scr = at.empty(n, torch.uint8, first.device) if n else None
     _check(lib.ag_resnorm_backward(op, _addr(X), _addr(B), _addr(G), _addr(dX), _addr(dZ),
                                    _addr(out["R"]), *[_addr(out.get(k)) for k in ("B", "G") + _NORM_VECTORS],
                                    N, H, code, _addr(scr), n, at.handle))

@@ -455,9 +455,8 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
         float2 st[n];
         float x[n], da[n];
 #pragma unroll
-        for (int s = 0; s < n; ++s) read(parity, s0 + s, q, a[s], b[s], st[s]);
-#pragma unroll
         for (int s = 0; s < n; ++s) {
+            read(parity, s0 + s, q, a[s], b[s], st[s]);
             x[s] = da[s] = 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) x[s] = F::dot(own_a[k], a[s][k], x[s]);
@@ -552,7 +551,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             const int count = P.heads - h0 < head_slots ? P.heads - h0 : head_slots;
             bits = 0;
             for (int o = 0; o < batch; o += group_lanes) {
-                const uint32_t k = keep_bits<1>(uint64_t(uint32_t(edge)) * uint32_t(P.heads) + uint32_t(h0), count, P.drop);
+                const uint32_t k = keep_bits<true>(uint64_t(uint32_t(edge)) * uint32_t(P.heads) + uint32_t(h0), count, P.drop);
                 for (int h = 0; h < head_slots; ++h) {
                     const uint32_t w = __ballot_sync(kAll, k >> h & 1u) >> group0;
                     if (h == hs) bits |= (group_lanes == 32 ? w : w & ((1u << group_lanes) - 1u)) << o;
@@ -797,8 +796,13 @@ void launch_walk(DiffParams &P, cudaStream_t st) {
     else k_diff_walk<T, VEC, DL, NV, MODE, false><<<grid, kWarps * 32, 0, st>>>(P);
 }
 
-// Vectors per map n = d / VEC: the next power of two of lanes up to 16, then
-// more vectors per lane.
+// Lanes and vectors per lane of a map's n = d / VEC vectors.  From eight
+// vectors of four features (sixteen of eight) on, two vectors a lane halve the
+// lanes of a score's sum: 564 K edges, fp32, 4 heads of 2 x 64: backward 992
+// -> 624 us, of 2 x 32: 419 -> 345 us.  Below, they only put more tiles, and
+// their row ends, into a warp: R-MAT-18, bf16, 4 heads of 2 x 16: forward 0.37
+// -> 0.75 ms, so one vector stays there.  Four vectors a lane (2 x 64, fp32)
+// measured 690 us against 624.
 template <typename T, int VEC, int MODE>
 void launch_vec(DiffParams &P, cudaStream_t st) {
     const int n = P.d / VEC;
@@ -812,8 +816,9 @@ void launch_vec(DiffParams &P, cudaStream_t st) {
         if (n <= 1) launch_walk<T, VEC, 1, 1, MODE>(P, st);
         else if (n <= 2) launch_walk<T, VEC, 2, 1, MODE>(P, st);
         else if (n <= 4) launch_walk<T, VEC, 4, 1, MODE>(P, st);
+        else if (VEC == 4 && n <= 8) launch_walk<T, VEC, 4, 2, MODE>(P, st);
         else if (n <= 8) launch_walk<T, VEC, 8, 1, MODE>(P, st);
-        else if (n <= 16) launch_walk<T, VEC, 16, 1, MODE>(P, st);
+        else if (n <= 16) launch_walk<T, VEC, 8, 2, MODE>(P, st);
         else if (n <= 32) launch_walk<T, VEC, 16, 2, MODE>(P, st);
         else launch_walk<T, VEC, 16, kWide, MODE>(P, st);
     }

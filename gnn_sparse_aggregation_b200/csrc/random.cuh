@@ -40,14 +40,15 @@ inline Drop make_drop(double p, uint64_t seed, uint64_t offset) {
 #ifdef __CUDACC__
 namespace {
 
-// UNROLL 10 where the blocks are the work; 1 inside a loop that has other
-// work, where the compiler would otherwise keep the ten rounds' keys in
-// registers across the loop (40 more in the attention's walks).
-template <int UNROLL = 10>
+// FRESH_KEYS: inside a loop that has other work the compiler would keep the
+// ten rounds' keys in registers across the loop (20 more); the key is made
+// opaque there, so that each block derives them anew.
+template <bool FRESH_KEYS = false>
 __device__ __forceinline__ uint4 philox(uint64_t block, const Drop &d) {
     uint32_t c0 = uint32_t(block), c1 = uint32_t(block >> 32), c2 = d.o0, c3 = d.o1;
     uint32_t k0 = d.k0, k1 = d.k1;
-#pragma unroll UNROLL
+    if (FRESH_KEYS) asm volatile("" : "+r"(k0), "+r"(k1));
+#pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t m0 = uint64_t(c0) * 0xD2511F53u, m1 = uint64_t(c2) * 0xCD9E8D57u;
         c0 = uint32_t(m1 >> 32) ^ c1 ^ k0;
@@ -61,21 +62,21 @@ __device__ __forceinline__ uint4 philox(uint64_t block, const Drop &d) {
 }
 
 // Bit j: whether element 4 block + j is kept.
-template <int UNROLL = 10>
+template <bool FRESH_KEYS = false>
 __device__ __forceinline__ uint32_t keep4(uint64_t block, const Drop &d) {
-    const uint4 w = philox<UNROLL>(block, d);
+    const uint4 w = philox<FRESH_KEYS>(block, d);
     return uint32_t(w.x >= d.threshold) | uint32_t(w.y >= d.threshold) << 1 | uint32_t(w.z >= d.threshold) << 2 |
            uint32_t(w.w >= d.threshold) << 3;
 }
 
 // Bit j: whether element i + j is kept, j < count <= 28.
-template <int UNROLL = 10>
+template <bool FRESH_KEYS = false>
 __device__ __forceinline__ uint32_t keep_bits(uint64_t i, int count, const Drop &d) {
     uint32_t bits = 0;
     const uint64_t last = (i + uint64_t(count) - 1) >> 2;
     int at = -int(i & 3);
     for (uint64_t b = i >> 2; b <= last; ++b, at += 4) {
-        const uint32_t k = keep4<UNROLL>(b, d);
+        const uint32_t k = keep4<FRESH_KEYS>(b, d);
         bits |= at >= 0 ? k << at : k >> -at;
     }
     return bits;
