@@ -233,55 +233,15 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     const int len = tile ? int(P.E - p0 < P.T ? P.E - p0 : P.T) : 0;
     const int steps = int(P.E - t0 * P.T < P.T ? P.E - t0 * P.T : P.T);  // the first group's: the longest
 
+    // Loads that wait on one another go out in three rounds: ids, first row and
+    // masks' edges; gathered rows and rows' ends; owner rows.
+    int r = tile ? P.tile_nz[t] : 0;
+    const int r_last = tile ? (t + 1 < P.n_tiles ? P.tile_nz[t + 1] : P.n_nz - 1) : 0;  // the row at the tile's end
     const float lam = live ? P.lam[head] : 0.f;
     const float sign = map ? -lam : 1.f;
-
-    // the open row, the next one with its owner rows, and the id and end of the one after
-    int r = tile ? P.tile_nz[t] : 0;
-    bool before = tile && P.nz_rowptr[r] < p0;
-    int row = 0, row_end, row_begin = 0;
-    int next_row = 0, next_end = 0x7fffffff, far_row = 0, far_end = 0x7fffffff;
-    raw own_a[NV], own_b[NV], pre_a[NV], pre_b[NV];
-    float own_lse = 0.f, pre_lse = 0.f;
-    auto load_owner = [&](int id, raw (&a)[NV], raw (&b)[NV], float &lse) {
-        load_row(P.own_a, id, a);
-        if (MODE != kFwd) load_row(P.own_b, id, b);
-        if (MODE == kDQ) lse = P.lse[int64_t(id) * P.heads * 2 + stat_col] * kLog2e;
-    };
-    auto meta = [&](int i, int &id, int &end) {  // row i of the rows with edges, if there is one
-        if (i < P.n_nz) {
-            id = __ldg(P.nz_rows + i);
-            end = int(__ldg(P.nz_rowptr + i + 1) - p0);
-        }
-    };
-    meta(r, row, row_end);
-    if (!tile) row_end = 0x7fffffff;
-    meta(r + 1, next_row, next_end);
-    meta(r + 2, far_row, far_end);
-    load_owner(row, own_a, own_b, own_lse);
-    load_owner(next_row, pre_a, pre_b, pre_lse);
-    if (tile) {
-        // the owner rows of the tile's further rows into L2: where rows are
-        // short, one opens every few positions
-        const int n = int(t + 1 < P.n_tiles ? P.tile_nz[t + 1] : P.n_nz - 1) - r;  // rows after the first
-        const int bytes = (P.heads - h0 < head_slots ? P.heads - h0 : head_slots) * 2 * P.d * int(sizeof(T));
-        for (int i = 2 + (lane & (group_lanes - 1)); i <= n; i += group_lanes) {
-            const int64_t at = (int64_t(P.nz_rows[r + i]) * P.H + int64_t(h0) * 2 * P.d) * int64_t(sizeof(T));
-            for (int o = 0; o < bytes; o += 128) {
-                prefetch_l2(static_cast<const char *>(P.own_a) + at + o);
-                if (MODE != kFwd) prefetch_l2(static_cast<const char *>(P.own_b) + at + o);
-            }
-        }
-    }
-
-    // kFwd: sums of p v for the own and the other map; kDQ: A, B; kDKV: dk, dv
-    Sums<VEC> acc[2][NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) acc[0][k].zero(), acc[1][k].zero();
-    float m = 0.f;            // kFwd: the reference of exp2(x - m); kDQ: c, the row's first da
-    float sum = 0.f;          // of exp2(x - m), or of alpha
-    float dsum = 0.f;         // kDQ: D'
-    bool first = true;        // the next position opens a row
+    const int gl = lane & (group_lanes - 1);
+    const int group0 = lane & ~(group_lanes - 1);
+    int edge = DROP && gl < len ? __ldg(P.order + p0 + gl) : 0;
 
     // ------------------------------------------------------------ the ring of gathered rows
     unsigned char *const ring = ring_mem[threadIdx.x >> 5];
@@ -368,6 +328,60 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             if (MODE == kDKV) st = __ldg(nbr_st + uint64_t(uint32_t(id)) * stat_row);
         }
     };
+
+    Ids ids = load_ids(0);
+    if (RING) {
+        const Ids second = load_ids(U), third = load_ids(2 * U);
+        fetch_unit(0, ids);
+        fetch_unit(1, second);
+        ids = third;
+    }
+
+    // the open row, the next one with its owner rows, and the id and end of the one after
+    bool before = tile && P.nz_rowptr[r] < p0;
+    int row = 0, row_end, row_begin = 0;
+    int next_row = 0, next_end = 0x7fffffff, far_row = 0, far_end = 0x7fffffff;
+    raw own_a[NV], own_b[NV], pre_a[NV], pre_b[NV];
+    float own_lse = 0.f, pre_lse = 0.f;
+    auto load_owner = [&](int id, raw (&a)[NV], raw (&b)[NV], float &lse) {
+        load_row(P.own_a, id, a);
+        if (MODE != kFwd) load_row(P.own_b, id, b);
+        if (MODE == kDQ) lse = P.lse[int64_t(id) * P.heads * 2 + stat_col] * kLog2e;
+    };
+    auto meta = [&](int i, int &id, int &end) {  // row i of the rows with edges, if there is one
+        if (i < P.n_nz) {
+            id = __ldg(P.nz_rows + i);
+            end = int(__ldg(P.nz_rowptr + i + 1) - p0);
+        }
+    };
+    meta(r, row, row_end);
+    if (!tile) row_end = 0x7fffffff;
+    meta(r + 1, next_row, next_end);
+    meta(r + 2, far_row, far_end);
+    load_owner(row, own_a, own_b, own_lse);
+    load_owner(next_row, pre_a, pre_b, pre_lse);
+    if (tile) {
+        // the owner rows of the tile's further rows into L2: where rows are
+        // short, one opens every few positions
+        const int n = r_last - r;  // rows after the first
+        const int bytes = (P.heads - h0 < head_slots ? P.heads - h0 : head_slots) * 2 * P.d * int(sizeof(T));
+        for (int i = 2 + gl; i <= n; i += group_lanes) {
+            const int64_t at = (int64_t(P.nz_rows[r + i]) * P.H + int64_t(h0) * 2 * P.d) * int64_t(sizeof(T));
+            for (int o = 0; o < bytes; o += 128) {
+                prefetch_l2(static_cast<const char *>(P.own_a) + at + o);
+                if (MODE != kFwd) prefetch_l2(static_cast<const char *>(P.own_b) + at + o);
+            }
+        }
+    }
+
+    // kFwd: sums of p v for the own and the other map; kDQ: A, B; kDKV: dk, dv
+    Sums<VEC> acc[2][NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) acc[0][k].zero(), acc[1][k].zero();
+    float m = 0.f;            // kFwd: the reference of exp2(x - m); kDQ: c, the row's first da
+    float sum = 0.f;          // of exp2(x - m), or of alpha
+    float dsum = 0.f;         // kDQ: D'
+    bool first = true;        // the next position opens a row
 
     // the open row's partial of this tile
     auto write_slot = [&](int64_t s) {
@@ -531,19 +545,9 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
         }
     };
 
-    Ids ids = load_ids(0);
-    if (RING) {
-        fetch_unit(0, ids);
-        ids = load_ids(U);
-        fetch_unit(1, ids);
-        ids = load_ids(2 * U);
-    }
     // keep bits of this lane's head: of `batch` positions from mask_at on
-    const int gl = lane & (group_lanes - 1);
-    const int group0 = lane & ~(group_lanes - 1);
     const int batch = group_lanes > U ? group_lanes : U;
     uint32_t bits = 0xffffffffu;
-    int edge = DROP && gl < len ? __ldg(P.order + p0 + gl) : 0;
     int stop = row_end < len || !tile ? row_end : len;  // the end of what is taken without a look
     for (int pos = 0; pos < steps; pos += U) {
         const int parity = pos / U & 1;
