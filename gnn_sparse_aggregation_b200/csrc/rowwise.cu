@@ -18,35 +18,25 @@ constexpr int kSMs = 148;
 
 // ---------------------------------------------------------------------------- dropout
 
-// y_i = keep_i x_i / (1 - p).  A thread takes kDropVecs vectors of VEC (a
-// multiple of 4) elements at a time, VEC / 4 Philox blocks each: the products
-// of one block run under the selections of another.
-constexpr int kDropVecs = 2;
-
+// y_i = keep_i x_i / (1 - p).  A thread takes VEC (a multiple of 4) elements at
+// a time: VEC / 4 Philox blocks.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_dropout(const T *__restrict__ x, T *__restrict__ y, int64_t n, const Drop drop) {
     using F = Frag<T, VEC>;
     const int64_t vecs = n / VEC;
-    const int64_t threads = int64_t(gridDim.x) * blockDim.x;
+    const int64_t stride = int64_t(gridDim.x) * blockDim.x;
     const int64_t i0 = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    for (int64_t i = i0; i < vecs; i += kDropVecs * threads) {
-        typename F::raw r[kDropVecs];
+    for (int64_t i = i0; i < vecs; i += stride) {
+        const typename F::raw r = F::load_stream(x + i * VEC);
+        uint32_t k[VEC / 4];
 #pragma unroll
-        for (int u = 0; u < kDropVecs; ++u)
-            r[u] = i + u * threads < vecs ? F::load_stream(x + (i + u * threads) * VEC) : F::zero();
-        uint32_t k[kDropVecs][VEC / 4];
+        for (int q = 0; q < VEC / 4; ++q) k[q] = keep4(uint64_t(i) * (VEC / 4) + q, drop);
+        float v[VEC];
+        F::unpack(r, v);
+        mul_all<VEC>(v, drop.scale);
 #pragma unroll
-        for (int q = 0; q < VEC / 4; ++q)
-#pragma unroll
-            for (int u = 0; u < kDropVecs; ++u) k[u][q] = keep4(uint64_t(i + u * threads) * (VEC / 4) + q, drop);
-#pragma unroll
-        for (int u = 0; u < kDropVecs; ++u) {
-            float v[VEC];
-            F::unpack(r[u], v);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) v[j] = k[u][j / 4] >> (j & 3) & 1u ? v[j] * drop.scale : 0.f;
-            if (i + u * threads < vecs) F::store(y + (i + u * threads) * VEC, v);
-        }
+        for (int j = 0; j < VEC; ++j) v[j] = k[j / 4] >> (j & 3) & 1u ? v[j] : 0.f;
+        F::store(y + i * VEC, v);
     }
     // the last n % VEC elements
     const int64_t i = vecs * VEC + i0;
@@ -83,7 +73,7 @@ void launch_dropout(const void *X, void *Y, int64_t n, const Drop &drop, cudaStr
     const T *x = static_cast<const T *>(X);
     T *y = static_cast<T *>(Y);
     if ((uintptr_t(X) | uintptr_t(Y)) % (VEC * sizeof(T)) == 0)
-        k_dropout<T, VEC><<<grid_of(n / VEC + 1, 256 * kDropVecs, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
+        k_dropout<T, VEC><<<grid_of(n / VEC + 1, 256, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
     else
         k_dropout_scalar<T><<<grid_of((n + 3) / 4, 256, kSMs * 64), 256, 0, st>>>(x, y, n, drop);
 }
@@ -267,12 +257,14 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2 *red) {
     return v;
 }
 
-// 1 / (1 + exp(-x)): off by at most (|x| + 4) 2^-24, relative
-__device__ __forceinline__ float sigmoid(float x) {
+// 1 / (1 + 2^y), and of y = -x log2(e) the logistic function: off by at most
+// (|x| + 4) 2^-24, relative
+__device__ __forceinline__ float logistic2(float y) {
     float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
     return __fdividef(1.f, 1.f + e);
 }
+__device__ __forceinline__ float sigmoid(float x) { return logistic2(x * -1.4426950408889634f); }
 
 // VEC values of a vector from column c on, or `none` where there is no vector
 template <int VEC>
@@ -400,11 +392,14 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_fwd(const NormPar
                 mul_all<VEC>(b[k], r);
                 fma_all<VEC>(b[k], g1[k], b1[k]);
                 if (P.G) {
+                    float s[VEC], none[VEC];
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        const float s = sigmoid(g[k][v]);
-                        b[k][v] *= P.silu ? g[k][v] * s : s;
-                    }
+                    for (int v = 0; v < VEC; ++v) s[v] = g[k][v], none[v] = -0.f;
+                    mul_all<VEC>(s, -1.4426950408889634f);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) s[v] = logistic2(s[v]);
+                    if (P.silu) fma_all<VEC>(s, g[k], none);
+                    fma_all<VEC>(b[k], s, none);
                 }
                 if (P.drop.on) {
                     const uint32_t kept = keep_vec<VEC>(uint64_t(at + c), P.drop);
