@@ -55,6 +55,11 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 2;            // warps per block
 constexpr int kMinBlocks = 8;        // per SM: at most 128 registers a thread
 constexpr int kResidentWarps = 148 * kMinBlocks * kWarps;
+// Tiles of the schedule are joined while that leaves kMergeWarps warps (1.75
+// times the resident ones: uneven tiles still fill in for one another).  564 K
+// edges, 8 heads of 2 x 32, bf16: forward 238 -> 145 us, backward 522 -> 364;
+// with one wave of warps in place of 1.75 R-MAT-18 takes 1.55 ms against 1.19.
+constexpr int kMergeWarps = 4144, kMaxWalkTile = 1024;
 constexpr int kZeroPerWarp = 32;     // rows without edges per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -83,6 +88,8 @@ struct DiffParams {
     int64_t N;
     int T, H, heads, d, hb_log2;
     int groups;                  // lane groups of a warp that walk a tile
+    int shift;                   // 2^shift tiles of the graph's schedule to one of the walk's
+    int64_t graph_tiles;
     float c2;                    // scale * log2(e)
     float scale;
     Drop drop;
@@ -235,8 +242,8 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
 
     // Loads that wait on one another go out in three rounds: ids, first row and
     // masks' edges; gathered rows and rows' ends; owner rows.
-    int r = tile ? P.tile_nz[t] : 0;
-    const int r_last = tile ? (t + 1 < P.n_tiles ? P.tile_nz[t + 1] : P.n_nz - 1) : 0;  // the row at the tile's end
+    int r = tile ? P.tile_nz[t << P.shift] : 0;
+    const int r_last = tile ? (t + 1 < P.n_tiles ? P.tile_nz[(t + 1) << P.shift] : P.n_nz - 1) : 0;  // the row at the tile's end
     const float lam = live ? P.lam[head] : 0.f;
     const float sign = map ? -lam : 1.f;
     const int gl = lane & (group_lanes - 1);
@@ -590,16 +597,23 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
 
 // Rows cut by tile boundaries: the partials of slot 2 first + 1 and of the
 // slots 2t of tiles first + 1 .. last, in one pass (statistics and columns
-// together, as a softmax that runs over the slots).  A row cut into many tiles
-// (those are listed first) takes a block: stripes of threads take every
-// stripes-th slot, then the stripes are joined in order.  Every other row
-// takes the lanes of its columns, which take the slots in order.  All orders
-// are fixed by the graph and the sizes.
+// together, as a softmax that runs over the slots).  Where the walk's tiles are
+// the schedule's, the schedule lists the cut rows, those of many tiles first;
+// where they are several of them, a row's lanes look at one tile boundary and
+// take the row that it is the first to cut.  A row of many slots takes a whole
+// block (one of the list's, or after the block's other rows): stripes of
+// threads take every stripes-th slot, then the stripes are joined in order.
+// Every other row takes the lanes of its columns, which take the slots in
+// order.  All orders are fixed by the graph and the sizes.
 constexpr int kFixThreads = 512;
+constexpr int kLongCut = 10;
 
 struct FixParams {
-    const int4 *spans;
+    const int4 *spans;           // the cut rows, or null: by boundary
     int64_t n_long, n_span;
+    const int32_t *tile_nz, *nz_rows, *nz_rowptr;
+    int64_t n_tiles;
+    int T, shift;
     const float *partial;
     int64_t slot;
     const float *lam, *lse;
@@ -617,9 +631,29 @@ struct Span {  // one cut row's slots, 0 .. n - 1
     const float *first, *rest;
     int64_t step;
     int n;
-    __device__ __forceinline__ Span(const FixParams &P, const int4 &sp)
-        : first(P.partial + (2 * int64_t(sp.y) + 1) * P.slot), rest(P.partial + 2 * int64_t(sp.y) * P.slot),
-          step(2 * P.slot), n(sp.z - sp.y + 1) {}
+    int row;
+    // span k of the list, or the row that boundary k (the first position of
+    // tile k) is the first to cut; n = 0 where there is none
+    __device__ __forceinline__ Span(const FixParams &P, int64_t k) : first(nullptr), rest(nullptr), step(2 * P.slot), n(0), row(0) {
+        int64_t from;
+        if (P.spans) {
+            if (k >= P.n_span) return;
+            const int4 sp = P.spans[k];
+            from = sp.y;
+            n = sp.z - sp.y + 1;
+            row = sp.x;
+        } else {
+            if (k < 1 || k >= P.n_tiles) return;
+            const int r = P.tile_nz[k << P.shift];
+            const int64_t start = P.nz_rowptr[r], end = P.nz_rowptr[r + 1];
+            if (start >= k * P.T || start < (k - 1) * P.T) return;
+            from = k - 1;
+            n = int((end - 1) / P.T - from) + 1;
+            row = P.nz_rows[r];
+        }
+        first = P.partial + (2 * from + 1) * P.slot;
+        rest = P.partial + 2 * from * P.slot;
+    }
     __device__ __forceinline__ const float *operator[](int i) const { return i == 0 ? first : rest + i * step; }
 };
 
@@ -692,7 +726,7 @@ __device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c
 }
 
 template <typename T, int MODE, int CV>
-__global__ void __launch_bounds__(kFixThreads) k_diff_fixup(const FixParams P) {
+__global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(const FixParams P) {
     constexpr int kWords = 2 * CV + (MODE == kFwd ? 4 : (MODE == kDQ ? 1 : 0));
     __shared__ float red[kWords][kFixThreads];
     if (MODE == kDKV && P.lam_blocks > 0 && blockIdx.x == gridDim.x - 1) {
@@ -702,14 +736,38 @@ __global__ void __launch_bounds__(kFixThreads) k_diff_fixup(const FixParams P) {
         if (threadIdx.x < P.heads) P.dlam[threadIdx.x] = float(-s);
         return;
     }
+    __shared__ int64_t later[kFixThreads];
+    __shared__ int n_later;
+    const bool listed = P.spans != nullptr, whole = listed && blockIdx.x < P.n_long;
+    if (threadIdx.x == 0) {
+        n_later = whole ? 1 : 0;
+        later[0] = blockIdx.x;
+    }
+    __syncthreads();
     const int q_at = 2 * P.H;  // a slot's statistics
     FixSums<MODE, CV> sum;
-    if (blockIdx.x < P.n_long) {
-        const int4 sp = P.spans[blockIdx.x];
-        const Span S(P, sp);
-        int cols = 1;
-        while (cols * CV < P.H && cols < kFixThreads) cols <<= 1;
-        const int stripes = kFixThreads / cols, stripe = threadIdx.x / cols, tc = threadIdx.x % cols;
+    if (!whole) {
+        const int lanes = 1 << P.lanes_log2, tc = threadIdx.x & (lanes - 1);
+        const int64_t block = listed ? blockIdx.x - P.n_long : blockIdx.x;
+        const int64_t k = (listed ? P.n_long : 1) + ((block * kFixThreads + threadIdx.x) >> P.lanes_log2);
+        const Span S(P, k);
+        if (!listed && S.n > kLongCut) {
+            if (tc == 0) later[atomicAdd(&n_later, 1)] = k;  // (in any order: each row by itself)
+        } else if (S.n > 0) {
+            for (int c = tc * CV; c < P.H; c += lanes * CV) {
+                const int head = c / (2 * P.d), map = c / P.d & 1, q = q_at + 2 * head;
+                sum.start(MODE == kDQ ? S[0][q + map] : 0.f);
+                sum.add_slots(P, S, 0, 1, c, q, map);
+                fix_store<T, MODE, CV>(P, S.row, c, head, map, sum);
+            }
+        }
+    }
+    __syncthreads();
+    int cols = 1;
+    while (cols * CV < P.H && cols < kFixThreads) cols <<= 1;
+    const int stripes = kFixThreads / cols, stripe = threadIdx.x / cols, tc = threadIdx.x % cols;
+    for (int j = 0; j < n_later; ++j) {
+        const Span S(P, later[j]);
         for (int c0 = 0; c0 < P.H; c0 += cols * CV) {
             const int c = c0 + tc * CV;
             const int head = c / (2 * P.d), map = c / P.d & 1, q = q_at + 2 * head;
@@ -739,22 +797,10 @@ __global__ void __launch_bounds__(kFixThreads) k_diff_fixup(const FixParams P) {
                     }
                     sum.add(t1, t2, 0.f, u, w);
                 }
-                fix_store<T, MODE, CV>(P, sp.x, c, head, map, sum);
+                fix_store<T, MODE, CV>(P, S.row, c, head, map, sum);
             }
             __syncthreads();
         }
-        return;
-    }
-    const int lanes = 1 << P.lanes_log2;
-    const int64_t s = P.n_long + (((int64_t(blockIdx.x) - P.n_long) * kFixThreads + threadIdx.x) >> P.lanes_log2);
-    if (s >= P.n_span) return;
-    const int4 sp = P.spans[s];
-    const Span S(P, sp);
-    for (int c = (threadIdx.x & (lanes - 1)) * CV; c < P.H; c += lanes * CV) {
-        const int head = c / (2 * P.d), map = c / P.d & 1, q = q_at + 2 * head;
-        sum.start(MODE == kDQ ? S[0][q + map] : 0.f);
-        sum.add_slots(P, S, 0, 1, c, q, map);
-        fix_store<T, MODE, CV>(P, sp.x, c, head, map, sum);
     }
 }
 
@@ -788,6 +834,10 @@ void launch_walk(DiffParams &P, cudaStream_t st) {
     // as many tiles per warp as there are groups, but fewer while that leaves
     // warps idle: a warp takes its groups' row ends one after another
     P.groups = 32 / (2 * DL << hb);
+    P.shift = 0;
+    while ((P.T << P.shift) < kMaxWalkTile && (P.graph_tiles >> (P.shift + 1)) / P.groups >= kMergeWarps) ++P.shift;
+    P.T <<= P.shift;
+    P.n_tiles = (P.graph_tiles + (int64_t(1) << P.shift) - 1) >> P.shift;
     while (P.groups > 1 && (P.n_tiles + P.groups - 1) / P.groups < kResidentWarps) P.groups >>= 1;
     const int tiles = kWarps * P.groups;  // per block
     P.tile_blocks = unsigned((P.n_tiles + tiles - 1) / tiles);
@@ -845,11 +895,18 @@ void launch_mode(DiffParams &P, int dtype, uintptr_t addresses, cudaStream_t st)
 
 template <int MODE>
 void launch_fixup(const Direction &D, const DiffParams &P, int dtype, float *dlam, cudaStream_t st) {
-    if (D.n_span == 0 && MODE != kDKV) return;
+    const bool cuts = P.n_tiles > 1 && D.n_span > 0;
+    if (!cuts && MODE != kDKV) return;
     FixParams F = {};
-    F.spans = D.spans;
+    F.spans = P.shift == 0 ? D.spans : nullptr;
     F.n_long = D.n_span_long;
     F.n_span = D.n_span;
+    F.tile_nz = D.tile_nz;
+    F.nz_rows = D.nz_rows;
+    F.nz_rowptr = D.nz_rowptr;
+    F.n_tiles = P.n_tiles;
+    F.T = P.T;
+    F.shift = P.shift;
     F.partial = P.partial;
     F.slot = P.slot;
     F.lam = P.lam;
@@ -871,7 +928,8 @@ void launch_fixup(const Direction &D, const DiffParams &P, int dtype, float *dla
     F.lanes_log2 = 0;
     while (F.lanes_log2 < 5 && (four ? 4 : 1) << F.lanes_log2 < F.H) ++F.lanes_log2;
     const int rows = kFixThreads >> F.lanes_log2;
-    const unsigned grid = unsigned(F.n_long + (F.n_span - F.n_long + rows - 1) / rows) + (MODE == kDKV ? 1 : 0);
+    const int64_t shorts = P.shift == 0 ? F.n_span - F.n_long : F.n_tiles - 1;
+    const unsigned grid = unsigned(cuts ? (P.shift == 0 ? F.n_long : 0) + (shorts + rows - 1) / rows : 0) + (MODE == kDKV ? 1 : 0);
     if (dtype == AG_F32) {
         if (four) k_diff_fixup<float, MODE, 4><<<grid, kFixThreads, 0, st>>>(F);
         else k_diff_fixup<float, MODE, 1><<<grid, kFixThreads, 0, st>>>(F);
@@ -891,7 +949,7 @@ void set_direction(DiffParams &P, const ag_graph *g, int dir) {
     P.zero_rows = D.zero_rows;
     P.n_nz = int(D.n_nz);
     P.n_zero = g->N - D.n_nz;
-    P.n_tiles = g->n_tiles;
+    P.n_tiles = P.graph_tiles = g->n_tiles;
     P.E = g->E;
     P.T = g->tile_edges;
 }

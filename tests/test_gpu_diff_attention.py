@@ -114,6 +114,18 @@ def test_rows_cut_by_many_tiles(agb, heads, d, dtype):
     assert g.stats["spanning_rows_f"] > g.stats["long_spanning_rows_f"]
 
 
+def test_joined_tiles_with_rows_cut_by_many_of_them(agb):
+    # enough edges for the walks to join the schedule's tiles, and hubs on both
+    # sides that are cut into more than ten of the joined ones
+    rng = np.random.default_rng(31)
+    N, E = 9000, 300000
+    src, dst = rng.integers(0, N, E), rng.integers(0, N - 50, E)
+    dst[rng.permutation(E)[:4000]] = 11
+    src[rng.permutation(E)[:5000]] = N - 1
+    g = _check(agb, src, dst, N, 1, 33, torch.float32, p=0.1, what="joined")
+    assert g.stats["tiles"] > 2 * 4144 and g.stats["max_degree_f"] > 10 * 2 * g.stats["tile_edges"]
+
+
 @pytest.mark.parametrize("name,dtype,heads,p", [("uniform", torch.float32, 1, 0.0), ("sbm", torch.float32, 2, 0.1),
                                                 ("rmat16", torch.bfloat16, 4, 0.1), ("twohop", torch.float32, 4, 0.0)])
 def test_configurations(agb, name, dtype, heads, p):
