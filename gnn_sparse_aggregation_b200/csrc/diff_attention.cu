@@ -46,6 +46,7 @@
 #include "aggraph.h"
 #include "frag.cuh"
 #include "internal.h"
+#include "operands.h"
 #include "random.cuh"
 
 namespace ag {
@@ -970,21 +971,6 @@ int check_diff(const ag_graph *g, int64_t H, int64_t heads, int dtype, float sca
         return fail(AG_ERR_WORKSPACE, "%s: scratch of %zu bytes, need %zu", fn, scratch_bytes, L->total);
     if (reinterpret_cast<uintptr_t>(scratch) % kAlign != 0)
         return fail(AG_ERR_WORKSPACE, "%s: scratch must be 256-byte aligned", fn);
-    return check_device_ptr(scratch, g->device, "scratch");
-}
-
-struct Named {
-    const void *p;
-    const char *name;
-};
-template <int K>
-int check_pointers(const Named (&a)[K], const ag_graph *g, int align, const char *fn) {
-    for (const Named &x : a) {
-        if (!x.p) return fail(AG_ERR_INVALID_ARG, "%s: null %s", fn, x.name);
-        if (reinterpret_cast<uintptr_t>(x.p) % uintptr_t(align) != 0)
-            return fail(AG_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", fn, x.name);
-        if (int rc = check_device_ptr(x.p, g->device, x.name)) return rc;
-    }
     return AG_OK;
 }
 
@@ -1025,9 +1011,10 @@ int ag_diff_attn_fwd(const ag_graph *g, const void *Q, const void *K, const void
     int rc = check_diff(g, H, heads, dtype, scale, p, scratch, scratch_bytes, fn, &L);
     if (rc != AG_OK) return rc;
     const int b = dtype == AG_F32 ? 4 : 2;
-    const Named feats[] = {{Q, "Q"}, {K, "K"}, {V, "V"}, {Y, "Y"}}, floats[] = {{lam, "lambda"}, {lse, "lse"}};
-    if ((rc = check_pointers(feats, g, b, fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(floats, g, 4, fn)) != AG_OK) return rc;
+    const size_t f = size_t(g->N) * size_t(H) * size_t(b), h = size_t(heads) * 4, s = size_t(g->N) * h * 2;
+    const Operand ops[] = {{Q, "Q", f, b, kIn}, {K, "K", f, b, kIn}, {V, "V", f, b, kIn}, {lam, "lambda", h, 4, kIn},
+                           {Y, "Y", f, b, kOut}, {lse, "lse", s, 4, kOut}, {scratch, "scratch", L.total, 1, kOut}};
+    if ((rc = check_operands(ops, g->device, false, fn)) != AG_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     DiffParams P = base_diff(g, H, heads, lam, scale, make_drop(p, seed, offset), static_cast<char *>(scratch), L);
     set_direction(P, g, 0);
@@ -1053,10 +1040,12 @@ int ag_diff_attn_backward(const ag_graph *g, const void *Q, const void *K, const
     int rc = check_diff(g, H, heads, dtype, scale, p, scratch, scratch_bytes, fn, &L);
     if (rc != AG_OK) return rc;
     const int b = dtype == AG_F32 ? 4 : 2;
-    const Named feats[] = {{Q, "Q"}, {K, "K"}, {V, "V"}, {dY, "dY"}, {dQ, "dQ"}, {dK, "dK"}, {dV, "dV"}};
-    const Named floats[] = {{lam, "lambda"}, {lse, "lse"}, {dlam, "dlambda"}};
-    if ((rc = check_pointers(feats, g, b, fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(floats, g, 4, fn)) != AG_OK) return rc;
+    const size_t f = size_t(g->N) * size_t(H) * size_t(b), h = size_t(heads) * 4, s = size_t(g->N) * h * 2;
+    const Operand ops[] = {{Q, "Q", f, b, kIn}, {K, "K", f, b, kIn}, {V, "V", f, b, kIn}, {dY, "dY", f, b, kIn},
+                           {lam, "lambda", h, 4, kIn}, {lse, "lse", s, 4, kIn}, {dQ, "dQ", f, b, kOut},
+                           {dK, "dK", f, b, kOut}, {dV, "dV", f, b, kOut}, {dlam, "dlambda", h, 4, kOut},
+                           {scratch, "scratch", L.total, 1, kOut}};
+    if ((rc = check_operands(ops, g->device, false, fn)) != AG_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     char *scr = static_cast<char *>(scratch);
     DiffParams P = base_diff(g, H, heads, lam, scale, make_drop(p, seed, offset), scr, L);

@@ -8,6 +8,7 @@
 #include "aggraph.h"
 #include "frag.cuh"
 #include "internal.h"
+#include "operands.h"
 #include "random.cuh"
 
 namespace ag {
@@ -690,32 +691,6 @@ void dispatch_norm(const NormParams &P, uintptr_t addresses, uintptr_t vectors, 
 
 // ---------------------------------------------------------------------------- checks
 
-struct Named {
-    const void *p;
-    const char *name;
-    bool need;
-};
-// Pointers of a call without a graph: device memory of the current device.
-template <int K>
-int check_pointers(const Named (&a)[K], const char *fn) {
-    int device = -1;
-    cudaError_t err = cudaGetDevice(&device);
-    if (err != cudaSuccess) return cuda_fail(err, fn);
-    for (const Named &x : a) {
-        if (!x.p) continue;
-        if (int rc = check_device_ptr(x.p, device, x.name)) return rc;
-    }
-    return AG_OK;
-}
-template <int K>
-int check_given(const Named (&a)[K], int align, const char *fn) {
-    for (const Named &x : a) {
-        if (x.need && !x.p) return fail(AG_ERR_INVALID_ARG, "%s: null %s", fn, x.name);
-        if (reinterpret_cast<uintptr_t>(x.p) % uintptr_t(align) != 0)
-            return fail(AG_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", fn, x.name);
-    }
-    return AG_OK;
-}
 int check_dtype(int dtype, const char *fn) {
     return dtype == AG_F32 || dtype == AG_BF16 ? int(AG_OK) : fail(AG_ERR_DTYPE, "%s: unknown dtype %d", fn, dtype);
 }
@@ -772,9 +747,9 @@ int ag_dropout(const void *X, void *Y, int64_t n, double p, uint64_t seed, uint6
     if ((rc = check_dtype(dtype, fn)) != AG_OK) return rc;
     if ((rc = check_drop(p, fn)) != AG_OK) return rc;
     if (n == 0) return AG_OK;
-    const Named a[] = {{X, "X", true}, {Y, "Y", true}};
-    if ((rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(a, fn)) != AG_OK) return rc;
+    const int b = element_size(dtype);
+    const Operand ops[] = {{X, "X", size_t(n) * size_t(b), b, kIn}, {Y, "Y", size_t(n) * size_t(b), b, kOut}};
+    if ((rc = check_operands(ops, kCurrent, true, fn)) != AG_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Drop drop = make_drop(p, seed, offset);
     if (dtype == AG_F32) launch_dropout<float, 4>(X, Y, n, drop, st);
@@ -831,12 +806,12 @@ int ag_rotary(const void *Q, const void *K, const int64_t *pos, const double *in
     if ((rc = check_dtype(dtype, fn)) != AG_OK) return rc;
     if (!isfinite(factor)) return fail(AG_ERR_INVALID_ARG, "%s: factor must be finite", fn);
     if (N == 0) return AG_OK;
-    const Named a[] = {{Q, "Q", true}, {Qo, "Q's output", true}, {K, "K", false}, {Ko, "K's output", K != nullptr}};
-    const Named b[] = {{pos, "pos", true}, {inv_freq, "inv_freq", true}};
-    if ((rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
-    if ((rc = check_given(b, 8, fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(a, fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(b, fn)) != AG_OK) return rc;
+    const int b = element_size(dtype);
+    const size_t f = size_t(N) * size_t(H) * size_t(b);
+    const Operand ops[] = {{Q, "Q", f, b, kIn}, {K, "K", f, b, kMaybeIn}, {pos, "pos", size_t(N) * 8, 8, kIn},
+                           {inv_freq, "inv_freq", size_t(rot) * 4, 8, kIn}, {Qo, "Q's output", f, b, kOut},
+                           {K ? Ko : nullptr, "K's output", f, b, K ? kOut : kMaybeOut}};
+    if ((rc = check_operands(ops, kCurrent, true, fn)) != AG_OK) return rc;
     RotaryParams P = {};
     P.in[0] = Q;
     P.in[1] = K;
@@ -872,13 +847,14 @@ int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, const voi
     if (!B && X) return fail(AG_ERR_INVALID_ARG, "%s: X without a block output (the sum is R)", fn);
     if (!B && !R) return fail(AG_ERR_INVALID_ARG, "%s: neither R nor B", fn);
     if (!X && !Z) return fail(AG_ERR_INVALID_ARG, "%s: neither X nor Z", fn);
-    const Named a[] = {{R, "R", false}, {B, "B", false}, {G, "G", false}, {X, "X", B != nullptr}, {Z, "Z", false}};
-    const Named f[] = {{op->gamma1, "gamma1", false}, {op->beta1, "beta1", false}, {op->scale, "scale", false},
-                       {op->gamma2, "gamma2", false}, {op->beta2, "beta2", false}};
-    if ((rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
-    if ((rc = check_given(f, 4, fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(a, fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(f, fn)) != AG_OK) return rc;
+    const int b = element_size(dtype);
+    const size_t f = size_t(N) * size_t(H) * size_t(b), h = size_t(H) * 4;
+    const Operand ops[] = {{R, "R", f, b, kMaybeIn}, {B, "B", f, b, kMaybeIn}, {G, "G", f, b, kMaybeIn},
+                           {X, "X", f, b, B ? kOut : kMaybeOut}, {Z, "Z", f, b, kMaybeOut},
+                           {op->gamma1, "gamma1", h, 4, kMaybeIn}, {op->beta1, "beta1", h, 4, kMaybeIn},
+                           {op->scale, "scale", h, 4, kMaybeIn}, {op->gamma2, "gamma2", h, 4, kMaybeIn},
+                           {op->beta2, "beta2", h, 4, kMaybeIn}};
+    if ((rc = check_operands(ops, kCurrent, true, fn)) != AG_OK) return rc;
     NormParams P = norm_params(op, N, H);
     P.R = R;
     P.B = B;
@@ -921,17 +897,19 @@ int ag_resnorm_backward(const ag_resnorm *op, const void *X, const void *B, cons
         return fail(AG_ERR_WORKSPACE, "%s: scratch of %zu bytes, need %zu", fn, scratch_bytes, need);
     if (reinterpret_cast<uintptr_t>(scratch) % kAlign != 0)
         return fail(AG_ERR_WORKSPACE, "%s: scratch must be 256-byte aligned", fn);
-    const Named a[] = {{X, "X", dZ != nullptr}, {B, "B", false}, {G, "G", false}, {dX, "dX", false}, {dZ, "dZ", false},
-                       {dR, "dR", false}, {dB, "dB", B != nullptr}, {dG, "dG", false}};
-    const Named f[] = {{op->gamma1, "gamma1", false}, {op->beta1, "beta1", false}, {op->scale, "scale", false},
-                       {op->gamma2, "gamma2", false}, {op->beta2, "beta2", false}, {dgamma1, "dgamma1", false},
-                       {dbeta1, "dbeta1", false}, {dscale, "dscale", false}, {dgamma2, "dgamma2", false},
-                       {dbeta2, "dbeta2", false}, {need ? scratch : nullptr, "scratch", false}};
+    const int b = element_size(dtype);
+    const size_t f = size_t(N) * size_t(H) * size_t(b), h = size_t(H) * 4;
+    const Operand ops[] = {{X, "X", f, b, N > 0 && dZ ? kIn : kMaybeIn}, {B, "B", f, b, kMaybeIn}, {G, "G", f, b, kMaybeIn},
+                           {dX, "dX", f, b, kMaybeIn}, {dZ, "dZ", f, b, kMaybeIn}, {dR, "dR", f, b, kMaybeOut},
+                           {dB, "dB", f, b, N > 0 && B ? kOut : kMaybeOut}, {dG, "dG", f, b, kMaybeOut},
+                           {op->gamma1, "gamma1", h, 4, kMaybeIn}, {op->beta1, "beta1", h, 4, kMaybeIn},
+                           {op->scale, "scale", h, 4, kMaybeIn}, {op->gamma2, "gamma2", h, 4, kMaybeIn},
+                           {op->beta2, "beta2", h, 4, kMaybeIn}, {dgamma1, "dgamma1", h, 4, kMaybeOut},
+                           {dbeta1, "dbeta1", h, 4, kMaybeOut}, {dscale, "dscale", h, 4, kMaybeOut},
+                           {dgamma2, "dgamma2", h, 4, kMaybeOut}, {dbeta2, "dbeta2", h, 4, kMaybeOut},
+                           {need ? scratch : nullptr, "scratch", need, 1, kMaybeOut}};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (N > 0 && (rc = check_given(a, element_size(dtype), fn)) != AG_OK) return rc;
-    if ((rc = check_given(f, 4, fn)) != AG_OK) return rc;
-    if (N > 0 && (rc = check_pointers(a, fn)) != AG_OK) return rc;
-    if ((rc = check_pointers(f, fn)) != AG_OK) return rc;
+    if ((rc = check_operands(ops, kCurrent, true, fn)) != AG_OK) return rc;
     int blocks = 0;
     if (N > 0) {
         NormParams P = norm_params(op, N, H);

@@ -349,7 +349,7 @@ AG_API int ag_attn_backward(const ag_graph *g, const void *Q, const void *K, con
  * per-edge weights [E] (dropped edges) i is the COO ordinal.  A new mask for
  * every step takes a new offset (or seed).
  *
- *   X, Y     device [n] of dtype; Y may be X
+ *   X, Y     device [n] of dtype; Y may be X (an overlap in part is refused)
  *   p        0 <= p < 1
  * Errors: AG_ERR_SHAPE (n outside [0, 2^40)), AG_ERR_DTYPE,
  * AG_ERR_INVALID_ARG (null or misaligned pointer, p outside [0, 1)),
@@ -371,7 +371,8 @@ AG_API int ag_dropout(const void *X, void *Y, int64_t n, double p, uint64_t seed
  *   Q, K       device [N, H] of dtype; K may be NULL (then Ko is ignored)
  *   pos        device int64 [N], any sign
  *   inv_freq   device double [rot / 2]
- *   Qo, Ko     device [N, H] of dtype; each may be its input
+ *   Qo, Ko     device [N, H] of dtype; each may be its input (other overlaps
+ *              are refused)
  *   heads      1 <= heads, H % heads == 0; for ag_diff_attn_* pass 2 * heads
  *              there, one for every map
  *   rot        even, 2 <= rot <= min(D, 4096)
@@ -428,7 +429,8 @@ AG_API int ag_rotary_freqs(int64_t rot, double base, int scaling, double factor,
  *            ag_diff_attn_scratch_bytes(g, H, heads) bytes (never O(E heads));
  *            its contents are scratch only: calls that may overlap take one each
  * Errors as ag_attn_fwd; AG_ERR_SHAPE for heads that do not fit H,
- * AG_ERR_INVALID_ARG also for p outside [0, 1) and misaligned pointers.
+ * AG_ERR_INVALID_ARG also for p outside [0, 1), misaligned pointers, and an
+ * output that overlaps an input or another output.
  */
 AG_API size_t ag_diff_attn_scratch_bytes(const ag_graph *g, int64_t H, int64_t heads);
 AG_API int ag_diff_attn_fwd(const ag_graph *g, const void *Q, const void *K, const void *V, const float *lam,
@@ -485,7 +487,8 @@ typedef struct ag_resnorm {
 
 /*
  *   R, B, G  device [N, H] of dtype
- *   X, Z     device [N, H] of dtype, fully written; X may be R, Z may be B
+ *   X, Z     device [N, H] of dtype, fully written; either may be an input
+ *            (overlaps in part, and of the two, are refused)
  *   N, H     0 <= N < 2^31, 1 <= H <= 8192
  * Errors: AG_ERR_SHAPE, AG_ERR_DTYPE, AG_ERR_INVALID_ARG (null op, X missing
  * with B, parts that do not go together, unknown norm or act, eps or p outside
@@ -507,7 +510,7 @@ AG_API int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, co
  *
  *   X        device [N, H] of dtype (needed with dZ)
  *   B, G     as in the forward call
- *   dR, dB, dG  device [N, H] of dtype; dR may be dX, dB may be B
+ *   dR, dB, dG  device [N, H] of dtype; each may be an input, as in the forward call
  *   dgamma1, dbeta1, dscale, dgamma2, dbeta2  device float [H], fully written
  *   scratch  device buffer, 256-byte aligned, of ag_resnorm_scratch_bytes(N, H)
  *            bytes; not needed without a column sum

@@ -269,3 +269,55 @@ def test_refusals(agb):
     assert call(H=17) == 2 and call(H=2 * 257, heads=1) == 2 and call(H=16, heads=0) == 2 and call(dtype=9) == 3
     assert agb.lib.ag_diff_attn_scratch_bytes(g.handle, 17, 2) == 0
     torch.cuda.synchronize()
+
+
+def test_outputs_that_overlap_are_refused(agb):
+    wl = workloads.make("uniform", seed=1, device=DEV)
+    g = agb.ag_graph_lower(wl.src, wl.dst, wl.N)
+    big = torch.zeros(2 * wl.X.numel(), device=DEV)
+    X, part = big[:wl.X.numel()].view_as(wl.X), big[16:16 + wl.X.numel()].view_as(wl.X)
+    X.copy_(wl.X)
+    lam = torch.ones(2, device=DEV)
+    other = torch.empty_like(X)
+    for Y in (X, part):
+        with pytest.raises(agb.AggraphError, match="overlaps"):
+            agb.ag_diff_attn_fwd(g, X, other.copy_(X), other, lam, 1.0, Y=Y)
+    _, lse = agb.ag_diff_attn_fwd(g, X, X, X, lam, 1.0)
+    for kw in (dict(dQ=X), dict(dV=part), dict(dQ=other, dK=other), dict(dlam=lam)):
+        with pytest.raises(agb.AggraphError, match="overlaps"):
+            agb.ag_diff_attn_backward(g, X, X, X, lam, 1.0, lse, X, **kw)
+    torch.cuda.synchronize()
+
+
+def test_rows_beyond_32_bit_offsets(agb):
+    # 2^24 + 512 rows of 256 bytes: the last nodes' rows lie past 2^32 bytes and 2^31
+    # elements.  The same small graph on the first nodes gives the same bits.
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    rng = np.random.default_rng(4)
+    n, N = 400, (1 << 24) + 512
+    src, dst = rng.integers(0, n, 5000), rng.integers(0, n - 9, 5000)
+    dst[:600] = 3
+    Q, K, V, G, lam = _tensors(n, 2, 32, torch.bfloat16, 5)
+    kw = dict(p=0.1, seed=3)
+
+    def run(src, dst, N, place):
+        g = agb.ag_graph_lower(*(torch.as_tensor(x.astype(np.int32)).to(DEV) for x in (src, dst)), N)
+        q, k, v, d = (place(t) for t in (Q, K, V, G))
+        Y, lse = agb.ag_diff_attn_fwd(g, q, k, v, lam, 0.2, **kw)
+        out = [Y[-n:].clone(), lse[-n:].clone()]
+        assert N == n or not Y[:1000].any() and torch.isinf(lse[:1000]).all()
+        del Y
+        dQ, dK, dV, dlam = agb.ag_diff_attn_backward(g, q, k, v, lam, 0.2, lse, d, **kw)
+        torch.cuda.synchronize()
+        return out + [dQ[-n:].clone(), dK[-n:].clone(), dV[-n:].clone(), dlam]
+
+    def high(t):
+        big = torch.zeros(N, t.shape[1], dtype=t.dtype, device=DEV)
+        big[-n:] = t
+        return big
+    low = run(src, dst, n, lambda t: t)
+    far = run(src + N - n, dst + N - n, N, high)
+    for a, b in zip(low[:-1], far[:-1]):
+        assert torch.equal(bits(a), bits(b))
+    torch.testing.assert_close(far[-1], low[-1], rtol=4 * lo.U, atol=0)   # fp64 sums in another order, rounded once

@@ -344,6 +344,46 @@ def test_rowwise_streams_and_capture(agb):
         assert all(torch.equal(bits(a), bits(b)) for a, b in zip(o, want))
 
 
+def test_rowwise_beyond_32_bit_offsets(agb):
+    # 2^31 + 24 elements of bf16: the last block's counters pass 2^29, offsets 2^32 bytes
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    n = (1 << 31) + 24
+    X = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    Y = agb.ag_dropout(X, 0.5, 5, 6)
+    for first in (0, (1 << 31) - 512, n - 1000):
+        some = host(Y[first:first + 1000])      # (fewer at the end)
+        assert np.array_equal(some != 0, lo.keep_mask(len(some), 0.5, 5, 6, first=first)), first
+    # the same rows at the end of a matrix and by themselves (the mask goes by the index: without dropout)
+    N, H = n // 8, 8
+    tail = workloads.features(64, H, torch.bfloat16, 3, DEV)
+    M = X.view(N, H)
+    M[-64:] = tail
+    _, Z = agb.ag_resnorm_fwd(M, None, norm="layer", Z=Y.view(N, H))
+    assert torch.equal(Z[-64:], agb.ag_resnorm_fwd(tail, None, norm="layer")[1])
+    freq = agb.ag_rotary_freqs(4)[0].to(DEV)
+    pos = torch.arange(N, device=DEV)
+    agb.ag_rotary(M, None, pos, freq, 2, Qo=M)
+    assert torch.equal(M[-64:], agb.ag_rotary(tail, None, pos[-64:].contiguous(), freq, 2)[0])
+
+
+def test_outputs_in_place_and_overlaps(agb):
+    N, H = 60, 32
+    m, v = _resnorm_case(N, H, torch.float32, 21)
+    want = agb.ag_resnorm_fwd(m["R"], m["B"], m["G"], p=0.1, **v)
+    R, B = m["R"].clone(), m["B"].clone()
+    got = agb.ag_resnorm_fwd(R, B, m["G"], p=0.1, X=R, Z=B, **v)
+    assert got[0] is R and got[1] is B and all(torch.equal(a, b) for a, b in zip(got, want))
+    big = torch.zeros(3 * N * H, device=DEV)
+    A, part = big[:N * H].view(N, H), big[H:H + N * H].view(N, H)
+    f, pos = torch.ones(4, dtype=torch.float64, device=DEV), torch.arange(N, device=DEV)
+    for call in (lambda: agb.ag_dropout(A, 0.1, 1, out=part), lambda: agb.ag_rotary(A, None, pos, f, 2, Qo=part),
+                 lambda: agb.ag_rotary(A, m["R"], pos, f, 2, Qo=m["B"], Ko=m["B"]),
+                 lambda: agb.ag_resnorm_fwd(A, m["B"], X=part), lambda: agb.ag_resnorm_fwd(A, m["B"], X=m["R"], Z=m["R"])):
+        with pytest.raises(agb.AggraphError, match="overlaps"):
+            call()
+
+
 def test_rowwise_refusals(agb):
     X = torch.randn(8, 16, device=DEV)
     f = torch.ones(4, dtype=torch.float64, device=DEV)
