@@ -25,8 +25,12 @@
 //                    known before the row's end, so the walk sums
 //                    A = sum alpha (da - c) k, B = sum alpha k and
 //                    D' = sum alpha (da - c) for a reference c (the row's
-//                    first da): dq = scale (A - D' B), D = c + D'.  The shift
-//                    by c keeps A and D' B from cancelling;
+//                    first da): dq = scale (A - D' B).  The shift by c keeps A
+//                    and D' B from cancelling where the da lie close together;
+//                    D itself is summed without it (da that lie around 0 would
+//                    lose to c + D').  The alphas are divided by their own sum:
+//                    the log-sum-exp is rounded, by up to 2.4e-7 between 4 and 8,
+//                    one factor for the whole row;
 //   kDKV             source rows of the transpose CSR; D known.
 // No per-edge array is written or read besides the CSR itself.
 //
@@ -389,6 +393,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     float m = 0.f;            // kFwd: the reference of exp2(x - m); kDQ: c, the row's first da
     float sum = 0.f;          // of exp2(x - m), or of alpha
     float dsum = 0.f;         // kDQ: D'
+    float draw = 0.f;         // kDQ: sum of alpha da
     bool first = true;        // the next position opens a row
 
     // the open row's partial of this tile
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             float *q = base + 2 * P.H + stat_col;
             q[0] = m;
             q[2 * P.heads] = sum;
-            if (MODE == kDQ) q[4 * P.heads] = dsum;
+            if (MODE == kDQ) q[4 * P.heads] = dsum, q[6 * P.heads] = draw;
         }
     };
     // writes the rows that end before position pos and opens the next ones (all lanes call it)
@@ -422,12 +427,13 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             own_w = sign * __fdividef(P.drop.scale, sum);  // (sum below 2^71)
             other_w = __shfl_xor_sync(kAll, own_w, DL);
         }
+        if (MODE == kDQ) other_w = __fdividef(1.f, sum);   // near 1: what the rounded log-sum-exp left
         if (!ends) return;
         if (before) {  // continued from the previous tile
             write_slot(2 * t);
             before = false;
         } else {
-            const float w = sign * P.scale;
+            const float w = sign * P.scale * other_w, dn = dsum * other_w;  // kDQ
             const int64_t at = int64_t(row) * P.H + col0;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     if (MODE == kFwd) u[i] = fmaf(u[i], own_w, v[i] * other_w);
-                    if (MODE == kDQ) u[i] = w * fmaf(-dsum, v[i], u[i]);
+                    if (MODE == kDQ) u[i] = w * fmaf(-dn, v[i], u[i]);
                 }
                 if (ok[k]) {
                     F::store(static_cast<T *>(P.out_a) + at + k * DL * VEC, u);
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             if (live && l == 0) {
                 const int64_t c = int64_t(row) * P.heads * 2 + stat_col;
                 if (MODE == kFwd) P.lse_out[c] = (m + log2f(sum)) * kLn2;
-                if (MODE == kDQ) P.stat[c] = make_float2(own_lse, m + dsum);
+                if (MODE == kDQ) P.stat[c] = make_float2(fmaf(sum - 1.f, kLog2e, own_lse), draw * other_w);
             }
         }
 #pragma unroll
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             acc[1][k].zero();
         }
         own_lse = pre_lse;
-        sum = dsum = 0.f;
+        sum = dsum = draw = 0.f;
         first = true;
         row = next_row;
         row_end = next_end;
@@ -528,9 +534,10 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             } else if (MODE == kDQ) {
                 f1 = ex2(fmaf(x[s], P.c2, -own_lse));
                 f0 = f1 * (da[s] - m);
-                if (!valid) f0 = f1 = 0.f;
+                if (!valid) f0 = f1 = da[s] = 0.f;
                 sum += f1;
                 dsum += f0;
+                draw = fmaf(f1, da[s], draw);
             } else {
                 const float p = sign * ex2(fmaf(x[s], P.c2, -st[s].x));
                 f1 = p + __shfl_xor_sync(kAll, p, DL);
@@ -659,8 +666,8 @@ struct Span {  // one cut row's slots, 0 .. n - 1
 };
 
 // A thread's sums over slots: CV columns of one map.  kFwd: s1, s2 the maps'
-// (maximum, sum), a, b their weighted sums; kDQ: s1 = (C, D'), a = A shifted
-// to C, b = B; kDKV: a, b.
+// (maximum, sum), a, b their weighted sums; kDQ: s1 = (C, D'), s2 = (the sums of
+// alpha, of alpha da), a = A shifted to C, b = B; kDKV: a, b.
 template <int MODE, int CV>
 struct FixSums {
     float2 s1, s2;
@@ -668,12 +675,12 @@ struct FixSums {
 
     __device__ __forceinline__ void start(float C) {
         s1 = MODE == kDQ ? make_float2(C, 0.f) : make_float2(-3.402823466e38f, 0.f);
-        s2 = s1;
+        s2 = MODE == kDQ ? make_float2(0.f, 0.f) : s1;
 #pragma unroll
         for (int v = 0; v < CV; ++v) a[v] = b[v] = 0.f;
     }
-    // the terms (t1, t2, u, w) of a slot or of another thread's sums; alpha: kDQ, the slot's sum of it
-    __device__ __forceinline__ void add(float2 t1, float2 t2, float alpha, const float (&u)[CV], const float (&w)[CV]) {
+    // the terms (t1, t2, u, w) of a slot or of another thread's sums
+    __device__ __forceinline__ void add(float2 t1, float2 t2, const float (&u)[CV], const float (&w)[CV]) {
         if (MODE == kFwd) {
             const float m1 = fmaxf(s1.x, t1.x), m2 = fmaxf(s2.x, t2.x);
             const float f1 = ex2(s1.x - m1), g1 = ex2(t1.x - m1), f2 = ex2(s2.x - m2), g2 = ex2(t2.x - m2);
@@ -683,7 +690,7 @@ struct FixSums {
             for (int v = 0; v < CV; ++v) a[v] = fmaf(a[v], f1, g1 * u[v]), b[v] = fmaf(b[v], f2, g2 * w[v]);
         } else {
             const float shift = MODE == kDQ ? t1.x - s1.x : 0.f;
-            if (MODE == kDQ) s1.y += fmaf(shift, alpha, t1.y);
+            if (MODE == kDQ) s1.y += fmaf(shift, t2.x, t1.y), s2.x += t2.x, s2.y += t2.y;
 #pragma unroll
             for (int v = 0; v < CV; ++v) a[v] += MODE == kDQ ? fmaf(shift, w[v], u[v]) : u[v], b[v] += w[v];
         }
@@ -697,9 +704,9 @@ struct FixSums {
             float u[CV], w[CV];
             Frag<float, CV>::unpack(Frag<float, CV>::load(p + c), u);
             Frag<float, CV>::unpack(Frag<float, CV>::load(p + c + P.H), w);
-            if (MODE == kFwd) add(make_float2(p[q], p[q + h2]), make_float2(p[q + 1], p[q + 1 + h2]), 0.f, u, w);
-            else if (MODE == kDQ) add(make_float2(p[q + map], p[q + map + 2 * h2]), s2, p[q + map + h2], u, w);
-            else add(s1, s2, 0.f, u, w);
+            if (MODE == kFwd) add(make_float2(p[q], p[q + h2]), make_float2(p[q + 1], p[q + 1 + h2]), u, w);
+            else if (MODE == kDQ) add(make_float2(p[q + map], p[q + map + 2 * h2]), make_float2(p[q + map + h2], p[q + map + 3 * h2]), u, w);
+            else add(s1, s2, u, w);
         }
     }
 };
@@ -710,7 +717,12 @@ __device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c
     const float lam = P.lam[head];
     float f = 1.f, g = 0.f;
     if (MODE == kFwd) f = __fdividef(P.drop_scale, s.s1.y), g = -lam * __fdividef(P.drop_scale, s.s2.y);
-    if (MODE == kDQ) f = (map ? -lam : 1.f) * P.scale, g = -s.s1.y * f;
+    if (MODE == kDQ) {
+        const float inv = __fdividef(1.f, s.s2.x);
+        s.s1.y *= inv;
+        f = (map ? -lam : 1.f) * P.scale * inv;
+        g = -s.s1.y * f;
+    }
     T *out = static_cast<T *>(P.out_a) + row * P.H + c;
     if (MODE != kDKV) {
 #pragma unroll
@@ -722,13 +734,13 @@ __device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c
         const int64_t k = (row * P.heads + head) * 2 + map;
         const float2 m = MODE == kFwd && map ? s.s2 : s.s1;
         if (MODE == kFwd) P.lse_out[k] = (m.x + log2f(m.y)) * kLn2;
-        if (MODE == kDQ) P.stat[k] = make_float2(P.lse[k] * kLog2e, m.x + m.y);
+        if (MODE == kDQ) P.stat[k] = make_float2(fmaf(s.s2.x - 1.f, kLog2e, P.lse[k] * kLog2e), __fdividef(s.s2.y, s.s2.x));
     }
 }
 
 template <typename T, int MODE, int CV>
 __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(const FixParams P) {
-    constexpr int kWords = 2 * CV + (MODE == kFwd ? 4 : (MODE == kDQ ? 1 : 0));
+    constexpr int kWords = 2 * CV + (MODE == kFwd ? 4 : (MODE == kDQ ? 3 : 0));
     __shared__ float red[kWords][kFixThreads];
     if (MODE == kDKV && P.lam_blocks > 0 && blockIdx.x == gridDim.x - 1) {
         __shared__ double sums[kFixThreads];
@@ -777,7 +789,7 @@ __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(
                 sum.add_slots(P, S, stripe, stripes, c, q, map);
 #pragma unroll
                 for (int v = 0; v < CV; ++v) red[v][threadIdx.x] = sum.a[v], red[CV + v][threadIdx.x] = sum.b[v];
-                if constexpr (MODE == kDQ) red[2 * CV][threadIdx.x] = sum.s1.y;
+                if constexpr (MODE == kDQ) red[2 * CV][threadIdx.x] = sum.s1.y, red[2 * CV + 1][threadIdx.x] = sum.s2.x, red[2 * CV + 2][threadIdx.x] = sum.s2.y;
                 if constexpr (MODE == kFwd) {
                     red[2 * CV][threadIdx.x] = sum.s1.x, red[2 * CV + 1][threadIdx.x] = sum.s1.y;
                     red[2 * CV + 2][threadIdx.x] = sum.s2.x, red[2 * CV + 3][threadIdx.x] = sum.s2.y;
@@ -791,12 +803,12 @@ __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(
 #pragma unroll
                     for (int v = 0; v < CV; ++v) u[v] = red[v][i], w[v] = red[CV + v][i];
                     float2 t1 = sum.s1, t2 = sum.s2;
-                    if constexpr (MODE == kDQ) t1.y = red[2 * CV][i];  // the same C
+                    if constexpr (MODE == kDQ) t1.y = red[2 * CV][i], t2 = make_float2(red[2 * CV + 1][i], red[2 * CV + 2][i]);  // (the same C)
                     if constexpr (MODE == kFwd) {
                         t1 = make_float2(red[2 * CV][i], red[2 * CV + 1][i]);
                         t2 = make_float2(red[2 * CV + 2][i], red[2 * CV + 3][i]);
                     }
-                    sum.add(t1, t2, 0.f, u, w);
+                    sum.add(t1, t2, u, w);
                 }
                 fix_store<T, MODE, CV>(P, S.row, c, head, map, sum);
             }
@@ -814,7 +826,7 @@ struct DiffLayout {
 };
 DiffLayout diff_layout(const ag_graph *g, int64_t H, int64_t heads) {
     DiffLayout L;
-    L.slot = (2 * H + 6 * heads + 3) / 4 * 4;
+    L.slot = (2 * H + 8 * heads + 3) / 4 * 4;
     const bool spans = g->dir[0].n_span > 0 || g->dir[1].n_span > 0;
     L.partial = 0;
     L.stat = align_up(spans ? size_t(2) * size_t(g->n_tiles) * size_t(L.slot) * 4 : 0);
