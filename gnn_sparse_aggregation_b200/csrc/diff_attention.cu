@@ -37,11 +37,28 @@
 // 2 DL lanes hold one head of one gathered row (DL lanes per map, NV vectors
 // of VEC features per lane), and as many heads as fit share a lane group of a
 // warp; each group walks a tile of T consecutive CSR positions of its own (the
-// tile schedule of the other aggregations), the wide heads of one row in
-// several groups.  A lane's columns of K belong to its own map; its columns of
-// V take the weights of both maps, the other one's by a shuffle.  Rows cut by
-// tile boundaries leave fp32 partials that a fix-up kernel adds in tile order,
-// so results are bitwise reproducible.
+// tile schedule of the other aggregations, joined where there are tiles to
+// spare); heads beyond a warp's lanes take further blocks.  A lane's columns of
+// K belong to its own map; its columns of V take the weights of both maps, the
+// other one's by a shuffle.  A group takes several positions at a time while
+// no group's row ends among them, and one position otherwise.  Gathered rows
+// come through a ring in shared memory by cp.async, each lane reading only what
+// it copied, so there is no barrier.  Rows cut by tile boundaries leave fp32
+// partials that a fix-up kernel adds in tile order: results are bitwise
+// reproducible.
+//
+// What bounds it: warp instructions, then the L2's rate for gathered rows
+// (15.1 TB/s for random 256-byte rows).  Every node of 64 edges, H = 128 bf16,
+// 4 heads, 4.2 M edges (two rows, so 512 bytes, per edge): forward 194 us = 11
+// TB/s at 63 warp instructions per two edges, 256 us with dropout (Philox, 23
+// more), dQ 236 us, dK and dV 282 us.  On R-MAT-18 (the same sizes, dropout)
+// 370 / 400 / 420 us: 15 % of the time the last tiles run alone, and rows of a
+// few edges cost about 120 instructions each.  Measured and not taken: a row
+// split over the lane groups of a warp with sums across them at its end (660 us
+// forward); tiles cut finer than the schedule's (a warp's first loads and its
+// partials cost about 4 us: 1.41 ms in place of 1.19 for the step); 32 lanes of
+// 8 bytes per row in place of 16 of 16 (1.54 ms); four tiles per warp (2.2 ms);
+// 96 registers and 20 warps per SM in place of 128 and 16 (1.24 ms).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
