@@ -82,6 +82,9 @@ constexpr int kResidentWarps = 148 * kMinBlocks * kWarps;
 // edges, 8 heads of 2 x 32, bf16: forward 238 -> 145 us, backward 522 -> 364;
 // with one wave of warps in place of 1.75 R-MAT-18 takes 1.55 ms against 1.19.
 constexpr int kMergeWarps = 4144, kMaxWalkTile = 1024;
+// Owner rows per lane of a group that go to L2 ahead (16.8 M rows of one edge,
+// H = 128 bf16: forward 4.86 ms, with all of a tile's 5.28).
+constexpr int kRowsAhead = 2;
 constexpr int kZeroPerWarp = 32;     // rows without edges per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -390,9 +393,9 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     load_owner(row, own_a, own_b, own_lse);
     load_owner(next_row, pre_a, pre_b, pre_lse);
     if (tile) {
-        // the owner rows of the tile's further rows into L2: where rows are
-        // short, one opens every few positions
-        const int n = r_last - r;  // rows after the first
+        // the owner rows of the tile's next rows into L2: where rows are short,
+        // one opens every few positions
+        const int n = r_last - r < kRowsAhead * group_lanes ? r_last - r : kRowsAhead * group_lanes;
         const int bytes = (P.heads - h0 < head_slots ? P.heads - h0 : head_slots) * 2 * P.d * int(sizeof(T));
         for (int i = 2 + gl; i <= n; i += group_lanes) {
             const int64_t at = (int64_t(P.nz_rows[r + i]) * P.H + int64_t(h0) * 2 * P.d) * int64_t(sizeof(T));
