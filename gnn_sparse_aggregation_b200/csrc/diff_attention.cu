@@ -67,6 +67,7 @@
 #include "aggraph.h"
 #include "frag.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "operands.h"
 #include "random.cuh"
 
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     constexpr int kRing = RING ? 2 * U * kPosBytes : 16;
     constexpr int kStatRing = RING && MODE == kDKV ? 2 * U * 32 * 8 : 0;
     __shared__ __align__(16) unsigned char ring_mem[kWarps][kRing + kStatRing];
+    follow_on();
     const int lane = threadIdx.x & 31;
     const int head_slots = 1 << P.hb_log2;
     const int group_lanes = HL << P.hb_log2;     // lanes that walk one tile
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
                 a[k] = ok[k] ? F::load(pa + k * DL * VEC) : F::zero();
                 b[k] = ok[k] ? F::load(pb + k * DL * VEC) : F::zero();
             }
-            if (MODE == kDKV) st = __ldg(nbr_st + uint64_t(uint32_t(id)) * stat_row);
+            if (MODE == kDKV) st = nbr_st[uint64_t(uint32_t(id)) * stat_row];  // (an earlier launch's: no __ldg)
         }
     };
 
@@ -722,8 +724,9 @@ struct FixSums {
         for (int i = i0; i < S.n; i += step) {
             const float *p = S[i];
             float u[CV], w[CV];
-            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c), u);
-            Frag<float, CV>::unpack(Frag<float, CV>::load(p + c + P.H), w);
+            using F = Frag<float, CV>;
+            F::unpack(F::load_written(p + c), u);
+            F::unpack(F::load_written(p + c + P.H), w);
             if (MODE == kFwd) add(make_float2(p[q], p[q + h2]), make_float2(p[q + 1], p[q + 1 + h2]), u, w);
             else if (MODE == kDQ) add(make_float2(p[q + map], p[q + map + 2 * h2]), make_float2(p[q + map + h2], p[q + map + 3 * h2]), u, w);
             else add(s1, s2, u, w);
@@ -762,6 +765,7 @@ template <typename T, int MODE, int CV>
 __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(const FixParams P) {
     constexpr int kWords = 2 * CV + (MODE == kFwd ? 4 : (MODE == kDQ ? 3 : 0));
     __shared__ float red[kWords][kFixThreads];
+    follow_on();
     if (MODE == kDKV && P.lam_blocks > 0 && blockIdx.x == gridDim.x - 1) {
         __shared__ double sums[kFixThreads];
         const double s = lam_sum(sums, kFixThreads, P.heads, P.lam_blocks, 0, 1,
@@ -879,8 +883,8 @@ void launch_walk(DiffParams &P, cudaStream_t st) {
     P.zero_blocks = unsigned(zero);
     const dim3 grid(P.tile_blocks + P.zero_blocks + (MODE == kDKV ? P.lam_blocks : 0), y);
     if (grid.x == 0) return;
-    if (P.drop.on) k_diff_walk<T, VEC, DL, NV, MODE, true><<<grid, kWarps * 32, 0, st>>>(P);
-    else k_diff_walk<T, VEC, DL, NV, MODE, false><<<grid, kWarps * 32, 0, st>>>(P);
+    if (P.drop.on) launch(k_diff_walk<T, VEC, DL, NV, MODE, true>, grid, kWarps * 32, MODE == kDKV, P, st);
+    else launch(k_diff_walk<T, VEC, DL, NV, MODE, false>, grid, kWarps * 32, MODE == kDKV, P, st);
 }
 
 // Lanes and vectors per lane of a map's n = d / VEC vectors.  From eight
@@ -964,11 +968,11 @@ void launch_fixup(const Direction &D, const DiffParams &P, int dtype, float *dla
     const int64_t shorts = P.shift == 0 ? F.n_span - F.n_long : F.n_tiles - 1;
     const unsigned grid = unsigned(cuts ? (P.shift == 0 ? F.n_long : 0) + (shorts + rows - 1) / rows : 0) + (MODE == kDKV ? 1 : 0);
     if (dtype == AG_F32) {
-        if (four) k_diff_fixup<float, MODE, 4><<<grid, kFixThreads, 0, st>>>(F);
-        else k_diff_fixup<float, MODE, 1><<<grid, kFixThreads, 0, st>>>(F);
+        if (four) launch(k_diff_fixup<float, MODE, 4>, dim3(grid), kFixThreads, true, F, st);
+        else launch(k_diff_fixup<float, MODE, 1>, dim3(grid), kFixThreads, true, F, st);
     } else {
-        if (four) k_diff_fixup<bf16_t, MODE, 4><<<grid, kFixThreads, 0, st>>>(F);
-        else k_diff_fixup<bf16_t, MODE, 1><<<grid, kFixThreads, 0, st>>>(F);
+        if (four) launch(k_diff_fixup<bf16_t, MODE, 4>, dim3(grid), kFixThreads, true, F, st);
+        else launch(k_diff_fixup<bf16_t, MODE, 1>, dim3(grid), kFixThreads, true, F, st);
     }
 }
 

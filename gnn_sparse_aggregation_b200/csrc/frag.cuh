@@ -32,6 +32,8 @@ template <typename T, int VEC> struct Frag {
     static __device__ __forceinline__ raw load(const T *p) { return __ldg(reinterpret_cast<const raw *>(p)); }
     // read once: does not displace what is read again
     static __device__ __forceinline__ raw load_stream(const T *p) { return __ldcs(reinterpret_cast<const raw *>(p)); }
+    // written by an earlier launch of the same call
+    static __device__ __forceinline__ raw load_written(const T *p) { return *reinterpret_cast<const raw *>(p); }
     static __device__ __forceinline__ void unpack(raw r, float (&v)[VEC]) {
         Bits b;
         if (kBytes < 4) b.w[0] = 0u;

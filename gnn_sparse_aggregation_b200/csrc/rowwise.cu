@@ -8,6 +8,7 @@
 #include "aggraph.h"
 #include "frag.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "operands.h"
 #include "random.cuh"
 
@@ -457,6 +458,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_bwd(const NormPar
     using F = Frag<T, VEC>;
     __shared__ float2 red[THREADS / 32];
     __shared__ float cols[RPB > 1 ? THREADS * VEC * NV : 1];
+    follow_on();
     const int l = threadIdx.x % TPR;
     bool ok[NV];
 #pragma unroll
@@ -626,6 +628,7 @@ struct JoinParams {
 // vector, its 32 warps each add every 32nd row, then the 32 in order.
 __global__ void __launch_bounds__(1024) k_resnorm_join(const JoinParams P) {
     __shared__ float red[32][33];
+    follow_on();
     float *out = P.out[blockIdx.y];
     if (!out) return;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -659,7 +662,7 @@ void launch_norm(const NormParams &P, int *blocks, cudaStream_t st) {
     constexpr int RPB = THREADS / TPR;
     if constexpr (BACK) {
         *blocks = int(grid_of(P.N, RPB, norm_blocks(P.N, P.H)));
-        k_resnorm_bwd<T, VEC, NV, TPR><<<*blocks, THREADS, 0, st>>>(P);
+        launch(k_resnorm_bwd<T, VEC, NV, TPR>, dim3(unsigned(*blocks)), THREADS, false, P, st);
     } else {
         k_resnorm_fwd<T, VEC, NV, TPR><<<grid_of(P.N, RPB, kSMs * 16), THREADS, 0, st>>>(P);
     }
@@ -945,7 +948,7 @@ int ag_resnorm_backward(const ag_resnorm *op, const void *X, const void *B, cons
         for (int k = 0; k < 5; ++k) J.out[k] = sums[k];
         J.blocks = blocks;
         J.H = int(H);
-        k_resnorm_join<<<dim3(unsigned((H + 31) / 32), 5), 1024, 0, st>>>(J);
+        launch(k_resnorm_join, dim3(unsigned((H + 31) / 32), 5), 1024, N > 0, J, st);
     }
     cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? AG_OK : cuda_fail(err, fn);

@@ -146,3 +146,42 @@ def test_layer_matches_autograd_and_its_captured_form():
     # (the library calls' bits are fixed; the projections between them may take another cuBLAS kernel under capture)
     for name, a, b in zip(("X1", "Z1") + GRADS, replayed, eager):
         assert float((a - b).abs().max()) <= 1e-3 * float(b.abs().max()), name
+
+
+def test_calls_in_a_row_share_memory_without_a_wait():
+    # outputs and scratch of one call are the next one's memory, each call's
+    # launches start as the one before runs out: eager and in one captured graph
+    # every call gives what it gives alone
+    agb = lib()
+    rng = np.random.default_rng(4)
+    N = 2000
+    src, dst = rng.integers(0, N, 30000), rng.integers(0, N, 30000)
+    dst[:5000], src[-4000:] = 17, 3       # rows of many tiles on both sides
+    g = agb.ag_graph_lower(*(torch.as_tensor(x.astype(np.int32)).to(DEV) for x in (src, dst)), N)
+    gen = torch.Generator().manual_seed(9)
+    sets = [[torch.randn(N, H, generator=gen).to(DEV) for _ in range(4)] for _ in range(2)]
+    lam = torch.full((HEADS,), 0.4, device=DEV)
+    ones = torch.ones(H, device=DEV)
+
+    def step(q, k, v, dy):
+        y, lse = agb.ag_diff_attn_fwd(g, q, k, v, lam, 0.3, p=PA, seed=SEED)
+        dq, dk, dv, dlam = agb.ag_diff_attn_backward(g, q, k, v, lam, 0.3, lse, dy, p=PA, seed=SEED)
+        back = agb.ag_resnorm_backward(v, y, k, dy, dq, gamma1=ones, scale=ones, gamma2=ones)
+        return [y, dq, dk, dv, dlam, *back.values()]
+
+    want = []
+    for s in sets:
+        want.append([x.clone() for x in step(*s)])
+        torch.cuda.synchronize()
+    got = [[x.clone() for x in step(*sets[i % 2])] for i in range(20)]
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i % 2], strict=True)), i
+    cg = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(cg):
+        kept = [[x.clone() for x in step(*sets[i % 2])] for i in range(6)]
+    for _ in range(5):
+        cg.replay()
+    torch.cuda.synchronize()
+    for i, r in enumerate(kept):
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i % 2], strict=True)), i
