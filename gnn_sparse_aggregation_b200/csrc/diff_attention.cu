@@ -24,9 +24,16 @@
 //   kDQ              destination rows; alpha from the log-sum-exp; D is not
 //                    known before the row's end, so the walk sums
 //                    A = sum alpha (da - c) k, B = sum alpha k and
-//                    D' = sum alpha (da - c) for a reference c (the row's
-//                    first da): dq = scale (A - D' B).  The shift by c keeps A
-//                    and D' B from cancelling where the da lie close together;
+//                    D' = sum alpha (da - c) for a reference c: dq = scale
+//                    (A - D' B).  The shift by c keeps A and D' B from cancelling
+//                    where the da lie close together, as long as c is the da of
+//                    what weighs in the row: |c| times the weight that it serves
+//                    then stays below a multiple of sum alpha |da|, whose rounding
+//                    every form of D has.  A row starts with its first da; where
+//                    the weight has grown beyond kRefWeight times the one that c
+//                    stands for, c moves, to the heaviest da of the new positions
+//                    if these outweigh all before, else to the mean so far, and
+//                    takes A and D' along (A += (c - c') B).
 //                    D itself is summed without it (da that lie around 0 would
 //                    lose to c + D').  The alphas are divided by their own sum:
 //                    the log-sum-exp is rounded, by up to 2.4e-7 between 4 and 8,
@@ -179,6 +186,12 @@ __device__ __forceinline__ double lam_sum(double *red, int threads, int heads, i
 // A running maximum is replaced only by a score beyond it by this much (in
 // powers of two): sums of exp2(x - m) stay below 2^(40 + 31).
 constexpr float kSlack = 40.f;
+
+// The weight that a row's reference c serves before it moves, over the weight
+// that it stands for.  At 32 a row of even weights moves it at its 33rd edge;
+// against a c that stays with the row's first edge: the step on 20 blocks 135.2
+// -> 137.4 us, two-hop 428 -> 428 us, R-MAT-18 1.18 -> 1.20 ms.
+constexpr float kRefWeight = 32.f;
 
 // Positions that a lane group takes at a time while no row ends among them.
 // Two such units are in flight: 8 KB of shared memory a warp.
@@ -412,8 +425,9 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     Sums<VEC> acc[2][NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) acc[0][k].zero(), acc[1][k].zero();
-    float m = 0.f;            // kFwd: the reference of exp2(x - m); kDQ: c, the row's first da
+    float m = 0.f;            // kFwd: the reference of exp2(x - m); kDQ: c
     float sum = 0.f;          // of exp2(x - m), or of alpha
+    float limit = 0.f;        // kDQ: the weight beyond which c moves
     float dsum = 0.f;         // kDQ: D'
     float draw = 0.f;         // kDQ: sum of alpha da
     bool first = true;        // the next position opens a row
@@ -544,7 +558,38 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
                 m = top;
             }
         }
-        if (MODE == kDQ && first) m = da[0];
+        float alpha[n];  // kDQ
+        if (MODE == kDQ) {
+            float w = 0.f;
+#pragma unroll
+            for (int s = 0; s < n; ++s) {
+                alpha[s] = ex2(fmaf(x[s], P.c2, -own_lse));
+                if (!valid) alpha[s] = da[s] = 0.f;
+                w += alpha[s];
+            }
+            if (first) m = da[0], limit = kRefWeight * alpha[0];
+            const float before_unit = sum;
+            sum += w;
+            if (sum > limit) {
+                float c = da[0], top = alpha[0];
+#pragma unroll
+                for (int s = 1; s < n; ++s) {
+                    c = alpha[s] > top ? da[s] : c;
+                    top = fmaxf(top, alpha[s]);
+                }
+                if (!(w > before_unit)) c = m + __fdividef(dsum, before_unit);
+                const float by = m - c;
+                dsum = fmaf(by, before_unit, dsum);
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    float u[VEC];
+                    acc[1][k].get(u);
+                    acc[0][k].add(Sums<VEC>::pair(by, by), u);
+                }
+                m = c;
+                limit = kRefWeight * sum;
+            }
+        }
         first = false;
 #pragma unroll
         for (int s = 0; s < n; ++s) {
@@ -554,10 +599,8 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
                 sum += f0;
                 f1 = __shfl_xor_sync(kAll, f0, DL);
             } else if (MODE == kDQ) {
-                f1 = ex2(fmaf(x[s], P.c2, -own_lse));
+                f1 = alpha[s];
                 f0 = f1 * (da[s] - m);
-                if (!valid) f0 = f1 = da[s] = 0.f;
-                sum += f1;
                 dsum += f0;
                 draw = fmaf(f1, da[s], draw);
             } else {
@@ -688,16 +731,15 @@ struct Span {  // one cut row's slots, 0 .. n - 1
 };
 
 // A thread's sums over slots: CV columns of one map.  kFwd: s1, s2 the maps'
-// (maximum, sum), a, b their weighted sums; kDQ: s1 = (C, D'), s2 = (the sums of
-// alpha, of alpha da), a = A shifted to C, b = B; kDKV: a, b.
+// (maximum, sum), a, b their weighted sums; kDQ: s1 = (c, D'), s2 = (the sums of
+// alpha, of alpha da), a = A about c, b = B; kDKV: a, b.
 template <int MODE, int CV>
 struct FixSums {
     float2 s1, s2;
     float a[CV], b[CV];
 
-    __device__ __forceinline__ void start(float C) {
-        s1 = MODE == kDQ ? make_float2(C, 0.f) : make_float2(-3.402823466e38f, 0.f);
-        s2 = MODE == kDQ ? make_float2(0.f, 0.f) : s1;
+    __device__ __forceinline__ void start() {
+        s1 = s2 = make_float2(MODE == kDQ ? 0.f : -3.402823466e38f, 0.f);
 #pragma unroll
         for (int v = 0; v < CV; ++v) a[v] = b[v] = 0.f;
     }
@@ -710,11 +752,16 @@ struct FixSums {
             s2 = make_float2(m2, fmaf(s2.y, f2, g2 * t2.y));
 #pragma unroll
             for (int v = 0; v < CV; ++v) a[v] = fmaf(a[v], f1, g1 * u[v]), b[v] = fmaf(b[v], f2, g2 * w[v]);
-        } else {
-            const float shift = MODE == kDQ ? t1.x - s1.x : 0.f;
-            if (MODE == kDQ) s1.y += fmaf(shift, t2.x, t1.y), s2.x += t2.x, s2.y += t2.y;
+        } else if (MODE == kDQ) {  // both about the mean da of the heavier
+            const float c = t2.x > s2.x ? t1.x + __fdividef(t1.y, t2.x) : s1.x + (s2.x > 0.f ? __fdividef(s1.y, s2.x) : 0.f);
+            const float p = s1.x - c, q = t1.x - c;
+            s1 = make_float2(c, fmaf(p, s2.x, s1.y) + fmaf(q, t2.x, t1.y));
+            s2.x += t2.x, s2.y += t2.y;
 #pragma unroll
-            for (int v = 0; v < CV; ++v) a[v] += MODE == kDQ ? fmaf(shift, w[v], u[v]) : u[v], b[v] += w[v];
+            for (int v = 0; v < CV; ++v) a[v] = fmaf(p, b[v], a[v]) + fmaf(q, w[v], u[v]), b[v] += w[v];
+        } else {
+#pragma unroll
+            for (int v = 0; v < CV; ++v) a[v] += u[v], b[v] += w[v];
         }
     }
     // slots i0, i0 + step, ...; q: where the head's statistics lie in a slot
@@ -763,7 +810,7 @@ __device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c
 
 template <typename T, int MODE, int CV>
 __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(const FixParams P) {
-    constexpr int kWords = 2 * CV + (MODE == kFwd ? 4 : (MODE == kDQ ? 3 : 0));
+    constexpr int kWords = 2 * CV + (MODE == kDKV ? 0 : 4);
     __shared__ float red[kWords][kFixThreads];
     follow_on();
     if (MODE == kDKV && P.lam_blocks > 0 && blockIdx.x == gridDim.x - 1) {
@@ -793,7 +840,7 @@ __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(
         } else if (S.n > 0) {
             for (int c = tc * CV; c < P.H; c += lanes * CV) {
                 const int head = c / (2 * P.d), map = c / P.d & 1, q = q_at + 2 * head;
-                sum.start(MODE == kDQ ? S[0][q + map] : 0.f);
+                sum.start();
                 sum.add_slots(P, S, 0, 1, c, q, map);
                 fix_store<T, MODE, CV>(P, S.row, c, head, map, sum);
             }
@@ -809,12 +856,11 @@ __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(
             const int c = c0 + tc * CV;
             const int head = c / (2 * P.d), map = c / P.d & 1, q = q_at + 2 * head;
             if (c < P.H) {
-                sum.start(MODE == kDQ ? S[0][q + map] : 0.f);
+                sum.start();
                 sum.add_slots(P, S, stripe, stripes, c, q, map);
 #pragma unroll
                 for (int v = 0; v < CV; ++v) red[v][threadIdx.x] = sum.a[v], red[CV + v][threadIdx.x] = sum.b[v];
-                if constexpr (MODE == kDQ) red[2 * CV][threadIdx.x] = sum.s1.y, red[2 * CV + 1][threadIdx.x] = sum.s2.x, red[2 * CV + 2][threadIdx.x] = sum.s2.y;
-                if constexpr (MODE == kFwd) {
+                if constexpr (MODE != kDKV) {
                     red[2 * CV][threadIdx.x] = sum.s1.x, red[2 * CV + 1][threadIdx.x] = sum.s1.y;
                     red[2 * CV + 2][threadIdx.x] = sum.s2.x, red[2 * CV + 3][threadIdx.x] = sum.s2.y;
                 }
@@ -827,8 +873,7 @@ __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(
 #pragma unroll
                     for (int v = 0; v < CV; ++v) u[v] = red[v][i], w[v] = red[CV + v][i];
                     float2 t1 = sum.s1, t2 = sum.s2;
-                    if constexpr (MODE == kDQ) t1.y = red[2 * CV][i], t2 = make_float2(red[2 * CV + 1][i], red[2 * CV + 2][i]);  // (the same C)
-                    if constexpr (MODE == kFwd) {
+                    if constexpr (MODE != kDKV) {
                         t1 = make_float2(red[2 * CV][i], red[2 * CV + 1][i]);
                         t2 = make_float2(red[2 * CV + 2][i], red[2 * CV + 3][i]);
                     }
