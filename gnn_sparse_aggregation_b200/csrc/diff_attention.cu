@@ -611,12 +611,12 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
                 if (DROP) f1 = kept >> s & 1u ? f1 * P.drop.scale : 0.f;
             }
             const uint64_t ff0 = Sums<VEC>::pair(f0, f0), ff1 = Sums<VEC>::pair(f1, f1);
-            // what is dropped (kFwd) or outside may hold infinities
-            const bool use = valid && (!DROP || MODE != kFwd || (kept >> s & 1u));
+            // what is outside may hold infinities, and the V (kFwd) or dY (kDKV) of what is dropped
+            const bool use = valid && (!DROP || (kept >> s & 1u));
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 float va[VEC], vb[VEC];
-                if (MODE != kFwd) F::unpack_if(a[s][k], use, va);
+                if (MODE != kFwd) F::unpack_if(a[s][k], valid, va);
                 if (MODE != kDQ) F::unpack_if(b[s][k], use, vb);
                 if (MODE == kFwd) acc[0][k].add(ff0, vb), acc[1][k].add(ff1, vb);
                 if (MODE == kDQ) acc[0][k].add(ff0, va), acc[1][k].add(ff1, va);
