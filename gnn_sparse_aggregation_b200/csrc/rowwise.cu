@@ -552,7 +552,10 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_resnorm_bwd(const NormPar
                 if (P.drop.on) {
                     const uint32_t kept = keep_vec<VEC>(uint64_t(at + c), P.drop);
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) dr[k][v] = kept >> v & 1u ? dr[k][v] * P.drop.scale : 0.f;
+                    for (int v = 0; v < VEC; ++v) {
+                        dr[k][v] = kept >> v & 1u ? dr[k][v] * P.drop.scale : 0.f;
+                        g[v] = kept >> v & 1u ? g[v] : 0.f;  // (0 times an infinite gate is no 0)
+                    }
                 }
                 if (!ok[k]) {
 #pragma unroll

@@ -90,3 +90,26 @@ def test_output_gradients_of_dropped_edges(agb, heads, d, dtype, value):
     torch.cuda.synchronize()
     assert torch.equal(want[2][clean], got[2][clean])
     assert not bool(torch.isfinite(got[2][reached].float()).all())
+
+
+@pytest.mark.parametrize("value", VALUES)
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("H,dtype", [(16, torch.float32), (33, torch.float32), (256, torch.float32), (2048, torch.float32),
+                                     (64, torch.bfloat16), (100, torch.bfloat16), (2050, torch.bfloat16), (8192, torch.bfloat16)])
+def test_gates_of_dropped_elements(agb, H, dtype, act, value):
+    # a gate that is infinite or NaN where its element is dropped: every output and gradient as with zeros there
+    N = 37
+    R, B, G, dX, dZ = (workloads.features(N, H, dtype, k, DEV) for k in range(5))
+    gen = torch.Generator().manual_seed(1)
+    v = {k: (0.5 + torch.rand(H, generator=gen)).to(DEV) for k in ("gamma1", "beta1", "scale", "gamma2", "beta2")}
+    kw = dict(norm="layer", act=act, p=0.3, seed=8, offset=1, **v)
+    gone = torch.as_tensor(~lo.keep_mask(N * H, 0.3, 8, 1).reshape(N, H)).to(DEV)
+    outs = []
+    for fill in (0.0, value):
+        G = torch.where(gone, torch.tensor(fill, dtype=dtype, device=DEV), G)
+        X, Z = agb.ag_resnorm_fwd(R, B, G, **kw)
+        d = agb.ag_resnorm_backward(X, B, G, dX, dZ, **kw)
+        outs.append([X, Z] + [d[k] for k in sorted(d)])
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        assert bool(torch.isfinite(a.float()).all()) and torch.equal(a, b)
