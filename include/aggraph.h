@@ -416,7 +416,8 @@ AG_API int ag_rotary_freqs(int64_t rot, double base, int scaling, double factor,
  *   lse_m[r]  = log of the sum over r's edges of exp(s_m)
  * u_e = 1, or with dropout (p > 0) keep / (1 - p): the mask of ag_dropout over
  * a COO-ordered [E, heads] array, one truth value for both maps.  Rows without
- * edges give Y = 0 and lse = -inf.  Scores, statistics and sums are fp32.
+ * edges give Y = 0 and lse = -inf.  Scores, statistics and sums are fp32: |V|
+ * times the row's edges has to stay below 2^119 (6e35).
  *
  *   Q, K, V  device [N, H] of dtype
  *   lam      device float [heads]
