@@ -12,7 +12,10 @@ namespace {
 
 constexpr int kCurrent = -1;
 
-enum Role { kIn, kMaybeIn, kOut, kMaybeOut };  // input, input that may be null, output, output that may be null
+// Inputs that a row-wise kernel reads an element of in the thread that writes
+// the output's (matrices), inputs that several rows read (parameters), outputs,
+// outputs of a launch that follows on all reads, and scratch.  Maybe: may be null.
+enum Role { kIn, kMaybeIn, kParam, kMaybeParam, kOut, kMaybeOut, kMaybeLast, kMaybeScratch };
 
 struct Operand {
     const void *p;
@@ -20,18 +23,24 @@ struct Operand {
     size_t bytes;
     int align;
     Role role;
-    bool output() const { return role == kOut || role == kMaybeOut; }
+    bool output() const { return role >= kOut; }
+    bool needed() const { return role == kIn || role == kParam || role == kOut; }
+    // whether this output may lie exactly where the input x does
+    bool in_place_of(const Operand &x) const {
+        if (x.output() || x.p != p || x.bytes != bytes || role == kMaybeScratch) return false;
+        return role == kMaybeLast || x.role == kIn || x.role == kMaybeIn;
+    }
 };
 
 // Every array given where it has to be, aligned to its elements, of `device`
 // (kCurrent: the calling thread's, for calls without a graph).
 // An output shares no memory with an output, and with an input none, or
-// (in_place) all of it: the row-wise kernels read an element before they write
-// it, in the thread that writes it.
+// (in_place) all of a matrix: the row-wise kernels read an element before they
+// write it, in the thread that writes it.
 template <int K>
 int check_operands(const Operand (&a)[K], int device, bool in_place, const char *fn) {
     for (const Operand &x : a) {
-        if (!x.p && (x.role == kIn || x.role == kOut)) return fail(AG_ERR_INVALID_ARG, "%s: null %s", fn, x.name);
+        if (!x.p && x.needed()) return fail(AG_ERR_INVALID_ARG, "%s: null %s", fn, x.name);
         if (reinterpret_cast<uintptr_t>(x.p) % uintptr_t(x.align) != 0)
             return fail(AG_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", fn, x.name);
     }
@@ -42,7 +51,7 @@ int check_operands(const Operand (&a)[K], int device, bool in_place, const char 
             if (j == i || !a[j].p) continue;
             const uintptr_t c = reinterpret_cast<uintptr_t>(a[j].p);
             if (b >= c + a[j].bytes || c >= b + a[i].bytes) continue;
-            if (in_place && !a[j].output() && b == c && a[i].bytes == a[j].bytes) continue;
+            if (in_place && a[i].in_place_of(a[j])) continue;
             return fail(AG_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, a[i].name, a[j].name);
         }
     }

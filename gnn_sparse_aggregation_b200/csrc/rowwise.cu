@@ -826,8 +826,8 @@ int ag_rotary(const void *Q, const void *K, const int64_t *pos, const double *in
     if (N == 0) return AG_OK;
     const int b = element_size(dtype);
     const size_t f = size_t(N) * size_t(H) * size_t(b);
-    const Operand ops[] = {{Q, "Q", f, b, kIn}, {K, "K", f, b, kMaybeIn}, {pos, "pos", size_t(N) * 8, 8, kIn},
-                           {inv_freq, "inv_freq", size_t(rot) * 4, 8, kIn}, {Qo, "Q's output", f, b, kOut},
+    const Operand ops[] = {{Q, "Q", f, b, kIn}, {K, "K", f, b, kMaybeIn}, {pos, "pos", size_t(N) * 8, 8, kParam},
+                           {inv_freq, "inv_freq", size_t(rot) * 4, 8, kParam}, {Qo, "Q's output", f, b, kOut},
                            {K ? Ko : nullptr, "K's output", f, b, K ? kOut : kMaybeOut}};
     if ((rc = check_operands(ops, kCurrent, true, fn)) != AG_OK) return rc;
     RotaryParams P = {};
@@ -869,9 +869,9 @@ int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, const voi
     const size_t f = size_t(N) * size_t(H) * size_t(b), h = size_t(H) * 4;
     const Operand ops[] = {{R, "R", f, b, kMaybeIn}, {B, "B", f, b, kMaybeIn}, {G, "G", f, b, kMaybeIn},
                            {X, "X", f, b, B ? kOut : kMaybeOut}, {Z, "Z", f, b, kMaybeOut},
-                           {op->gamma1, "gamma1", h, 4, kMaybeIn}, {op->beta1, "beta1", h, 4, kMaybeIn},
-                           {op->scale, "scale", h, 4, kMaybeIn}, {op->gamma2, "gamma2", h, 4, kMaybeIn},
-                           {op->beta2, "beta2", h, 4, kMaybeIn}};
+                           {op->gamma1, "gamma1", h, 4, kMaybeParam}, {op->beta1, "beta1", h, 4, kMaybeParam},
+                           {op->scale, "scale", h, 4, kMaybeParam}, {op->gamma2, "gamma2", h, 4, kMaybeParam},
+                           {op->beta2, "beta2", h, 4, kMaybeParam}};
     if ((rc = check_operands(ops, kCurrent, true, fn)) != AG_OK) return rc;
     NormParams P = norm_params(op, N, H);
     P.R = R;
@@ -920,12 +920,12 @@ int ag_resnorm_backward(const ag_resnorm *op, const void *X, const void *B, cons
     const Operand ops[] = {{X, "X", f, b, N > 0 && dZ ? kIn : kMaybeIn}, {B, "B", f, b, kMaybeIn}, {G, "G", f, b, kMaybeIn},
                            {dX, "dX", f, b, kMaybeIn}, {dZ, "dZ", f, b, kMaybeIn}, {dR, "dR", f, b, kMaybeOut},
                            {dB, "dB", f, b, N > 0 && B ? kOut : kMaybeOut}, {dG, "dG", f, b, kMaybeOut},
-                           {op->gamma1, "gamma1", h, 4, kMaybeIn}, {op->beta1, "beta1", h, 4, kMaybeIn},
-                           {op->scale, "scale", h, 4, kMaybeIn}, {op->gamma2, "gamma2", h, 4, kMaybeIn},
-                           {op->beta2, "beta2", h, 4, kMaybeIn}, {dgamma1, "dgamma1", h, 4, kMaybeOut},
-                           {dbeta1, "dbeta1", h, 4, kMaybeOut}, {dscale, "dscale", h, 4, kMaybeOut},
-                           {dgamma2, "dgamma2", h, 4, kMaybeOut}, {dbeta2, "dbeta2", h, 4, kMaybeOut},
-                           {need ? scratch : nullptr, "scratch", need, 1, kMaybeOut}};
+                           {op->gamma1, "gamma1", h, 4, kMaybeParam}, {op->beta1, "beta1", h, 4, kMaybeParam},
+                           {op->scale, "scale", h, 4, kMaybeParam}, {op->gamma2, "gamma2", h, 4, kMaybeParam},
+                           {op->beta2, "beta2", h, 4, kMaybeParam}, {dgamma1, "dgamma1", h, 4, kMaybeLast},
+                           {dbeta1, "dbeta1", h, 4, kMaybeLast}, {dscale, "dscale", h, 4, kMaybeLast},
+                           {dgamma2, "dgamma2", h, 4, kMaybeLast}, {dbeta2, "dbeta2", h, 4, kMaybeLast},
+                           {need ? scratch : nullptr, "scratch", need, 1, kMaybeScratch}};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((rc = check_operands(ops, kCurrent, true, fn)) != AG_OK) return rc;
     int blocks = 0;

@@ -371,8 +371,8 @@ AG_API int ag_dropout(const void *X, void *Y, int64_t n, double p, uint64_t seed
  *   Q, K       device [N, H] of dtype; K may be NULL (then Ko is ignored)
  *   pos        device int64 [N], any sign
  *   inv_freq   device double [rot / 2]
- *   Qo, Ko     device [N, H] of dtype; each may be its input (other overlaps
- *              are refused)
+ *   Qo, Ko     device [N, H] of dtype; each may be Q or K (in part, with pos or
+ *              inv_freq, or with one another they may not overlap)
  *   heads      1 <= heads, H % heads == 0; for ag_diff_attn_* pass 2 * heads
  *              there, one for every map
  *   rot        even, 2 <= rot <= min(D, 4096)
@@ -488,8 +488,8 @@ typedef struct ag_resnorm {
 
 /*
  *   R, B, G  device [N, H] of dtype
- *   X, Z     device [N, H] of dtype, fully written; either may be an input
- *            (overlaps in part, and of the two, are refused)
+ *   X, Z     device [N, H] of dtype, fully written; either may be R, B or G
+ *            (overlaps in part, of the two, and with a vector, are refused)
  *   N, H     0 <= N < 2^31, 1 <= H <= 8192
  * Errors: AG_ERR_SHAPE, AG_ERR_DTYPE, AG_ERR_INVALID_ARG (null op, X missing
  * with B, parts that do not go together, unknown norm or act, eps or p outside
@@ -511,7 +511,7 @@ AG_API int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, co
  *
  *   X        device [N, H] of dtype (needed with dZ)
  *   B, G     as in the forward call
- *   dR, dB, dG  device [N, H] of dtype; each may be an input, as in the forward call
+ *   dR, dB, dG  device [N, H] of dtype; each may be an input matrix, as in the forward call
  *   dgamma1, dbeta1, dscale, dgamma2, dbeta2  device float [H], fully written
  *   scratch  device buffer, 256-byte aligned, of ag_resnorm_scratch_bytes(N, H)
  *            bytes; not needed without a column sum
