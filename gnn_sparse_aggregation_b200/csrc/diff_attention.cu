@@ -957,8 +957,7 @@ void launch_vec(DiffParams &P, cudaStream_t st) {
         if (n <= 1) launch_walk<T, VEC, 1, 1, MODE>(P, st);
         else if (n <= 2) launch_walk<T, VEC, 2, 1, MODE>(P, st);
         else if (n <= 4) launch_walk<T, VEC, 4, 1, MODE>(P, st);
-        else if (VEC == 4 && n <= 8) launch_walk<T, VEC, 4, 2, MODE>(P, st);
-        else if (n <= 8) launch_walk<T, VEC, 8, 1, MODE>(P, st);
+        else if (n <= 8) launch_walk<T, VEC, VEC == 4 ? 4 : 8, VEC == 4 ? 2 : 1, MODE>(P, st);
         else if (n <= 16) launch_walk<T, VEC, 8, 2, MODE>(P, st);
         else if (n <= 32) launch_walk<T, VEC, 16, 2, MODE>(P, st);
         else launch_walk<T, VEC, 16, kWide, MODE>(P, st);

@@ -686,8 +686,7 @@ void dispatch_norm(const NormParams &P, int *blocks, cudaStream_t st) {
         else if (n <= 8) launch_norm<T, VEC, 1, 8, BACK>(P, blocks, st);
         else if (n <= 16) launch_norm<T, VEC, 1, 16, BACK>(P, blocks, st);
         else if (n <= 32) launch_norm<T, VEC, 1, 32, BACK>(P, blocks, st);
-        else if (VEC == 4 && n <= 64) launch_norm<T, VEC, VEC == 4 ? 2 : 1, VEC == 4 ? 32 : 64, BACK>(P, blocks, st);
-        else if (VEC == 8 && n <= 64) launch_norm<T, VEC, 1, 64, BACK>(P, blocks, st);
+        else if (n <= 64) launch_norm<T, VEC, VEC == 4 ? 2 : 1, VEC == 4 ? 32 : 64, BACK>(P, blocks, st);
         else if (n <= 128) launch_norm<T, VEC, 1, 128, BACK>(P, blocks, st);
         else if (n <= 256) launch_norm<T, VEC, 1, 256, BACK>(P, blocks, st);
         else if (n <= 512) launch_norm<T, VEC, 1, 512, BACK>(P, blocks, st);
