@@ -23,19 +23,13 @@
 //                    at the row's end), log-sum-exp written for the backward;
 //   kDQ              destination rows; alpha from the log-sum-exp; D is not
 //                    known before the row's end, so the walk sums
-//                    A = sum alpha (da - c) k, B = sum alpha k and
-//                    D' = sum alpha (da - c) for a reference c: dq = scale
-//                    (A - D' B).  The shift by c keeps A and D' B from cancelling
-//                    where the da lie close together, as long as c is the da of
-//                    what weighs in the row: |c| times the weight that it serves
-//                    then stays below a multiple of sum alpha |da|, whose rounding
-//                    every form of D has.  A row starts with its first da; where
-//                    the weight has grown beyond kRefWeight times the one that c
-//                    stands for, c moves, to the heaviest da of the new positions
-//                    if these outweigh all before, else to the mean so far, and
-//                    takes A and D' along (A += (c - c') B).
-//                    D itself is summed without it (da that lie around 0 would
-//                    lose to c + D').  The alphas are divided by their own sum:
+//                    A = sum alpha da k, B = sum alpha k and D = sum alpha da:
+//                    dq = scale (A - D B).  What A and D B have in common is of
+//                    the size of sum alpha |da|, whose rounding D has in any form,
+//                    so the difference costs no digits that ds = alpha (da - D)
+//                    would keep.  (Sums about a reference c in place of 0 would,
+//                    where c is the da of an edge of little weight.)  A row of one
+//                    edge has dq = 0.  The alphas are divided by their own sum:
 //                    the log-sum-exp is rounded, by up to 2.4e-7 between 4 and 8,
 //                    one factor for the whole row;
 //   kDKV             source rows of the transpose CSR; D known.
@@ -188,15 +182,9 @@ __device__ __forceinline__ double lam_sum(double *red, int threads, int heads, i
 // ever.  The sums hold up to 2^kSlack times the values: V times the row's edges
 // has to stay 2^8 below the largest number, and sums of exp2(x - m) stay below
 // 2^(8 + 31).  A slack of 40, which costs 32 more powers of two of V, measured
-// the same (training steps: 20 blocks 137.4 us, two-hop 427 us, R-MAT-18 1.20 to
-// 1.22 ms with both).
+// the same (training steps on 20 blocks and two-hop within 0.1 %, on R-MAT-18
+// within their spread of 1.5 %).
 constexpr float kSlack = 8.f;
-
-// The weight that a row's reference c serves before it moves, over the weight
-// that it stands for.  At 32 a row of even weights moves it at its 33rd edge;
-// against a c that stays with the row's first edge: the step on 20 blocks 135.2
-// -> 137.4 us, two-hop 428 -> 428 us, R-MAT-18 1.18 -> 1.20 ms.
-constexpr float kRefWeight = 32.f;
 
 // Positions that a lane group takes at a time while no row ends among them.
 // Two such units are in flight: 8 KB of shared memory a warp.
@@ -430,11 +418,9 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
     Sums<VEC> acc[2][NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) acc[0][k].zero(), acc[1][k].zero();
-    float m = 0.f;            // kFwd: the reference of exp2(x - m); kDQ: c
+    float m = 0.f;            // kFwd: the reference of exp2(x - m)
     float sum = 0.f;          // of exp2(x - m), or of alpha
-    float limit = 0.f;        // kDQ: the weight beyond which c moves
-    float dsum = 0.f;         // kDQ: D'
-    float draw = 0.f;         // kDQ: sum of alpha da
+    float dsum = 0.f;         // kDQ: sum of alpha da
     bool first = true;        // the next position opens a row
 
     // the open row's partial of this tile
@@ -456,9 +442,8 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
         }
         if (MODE != kDKV && l == 0) {
             float *q = base + 2 * P.H + stat_col;
-            q[0] = m;
+            q[0] = MODE == kFwd ? m : dsum;
             q[2 * P.heads] = sum;
-            if (MODE == kDQ) q[4 * P.heads] = dsum, q[6 * P.heads] = draw;
         }
     };
     // writes the rows that end before position pos and opens the next ones (all lanes call it)
@@ -474,7 +459,8 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             write_slot(2 * t);
             before = false;
         } else {
-            const float w = sign * P.scale * other_w, dn = dsum * other_w;  // kDQ
+            const bool lone = pos - row_begin == 1;
+            const float w = lone ? 0.f : sign * P.scale * other_w, D = dsum * other_w;  // kDQ
             const int64_t at = int64_t(row) * P.H + col0;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -484,7 +470,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     if (MODE == kFwd) u[i] = fmaf(u[i], own_w, v[i] * other_w);
-                    if (MODE == kDQ) u[i] = w * fmaf(-dn, v[i], u[i]);
+                    if (MODE == kDQ) u[i] = w * fmaf(-D, v[i], u[i]);
                 }
                 if (ok[k]) {
                     F::store(static_cast<T *>(P.out_a) + at + k * DL * VEC, u);
@@ -494,7 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             if (live && l == 0) {
                 const int64_t c = int64_t(row) * P.heads * 2 + stat_col;
                 if (MODE == kFwd) P.lse_out[c] = (m + log2f(sum)) * kLn2;
-                if (MODE == kDQ) P.stat[c] = make_float2(fmaf(sum - 1.f, kLog2e, own_lse), draw * other_w);
+                if (MODE == kDQ) P.stat[c] = make_float2(fmaf(sum - 1.f, kLog2e, own_lse), D);
             }
         }
 #pragma unroll
@@ -505,7 +491,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
             acc[1][k].zero();
         }
         own_lse = pre_lse;
-        sum = dsum = draw = 0.f;
+        sum = dsum = 0.f;
         first = true;
         row = next_row;
         row_end = next_end;
@@ -517,7 +503,7 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
         meta(r + 2, far_row, far_end);
     };
     // n positions of the unit, from s on, none of which opens a row but the
-    // first; in the group's range where valid (kFwd, kDQ: -inf and 0 outside)
+    // first; in the group's range where valid (kFwd: scores of -inf outside, else factors of 0)
     auto take = [&](auto count, int parity, int s0, const Ids &q, uint32_t kept, bool valid) {
         constexpr int n = decltype(count)::value;
         raw a[n][NV], b[n][NV];
@@ -563,38 +549,6 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
                 m = top;
             }
         }
-        float alpha[n];  // kDQ
-        if (MODE == kDQ) {
-            float w = 0.f;
-#pragma unroll
-            for (int s = 0; s < n; ++s) {
-                alpha[s] = ex2(fmaf(x[s], P.c2, -own_lse));
-                if (!valid) alpha[s] = da[s] = 0.f;
-                w += alpha[s];
-            }
-            if (first) m = da[0], limit = kRefWeight * alpha[0];
-            const float before_unit = sum;
-            sum += w;
-            if (sum > limit) {
-                float c = da[0], top = alpha[0];
-#pragma unroll
-                for (int s = 1; s < n; ++s) {
-                    c = alpha[s] > top ? da[s] : c;
-                    top = fmaxf(top, alpha[s]);
-                }
-                if (!(w > before_unit)) c = m + __fdividef(dsum, before_unit);
-                const float by = m - c;
-                dsum = fmaf(by, before_unit, dsum);
-#pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    float u[VEC];
-                    acc[1][k].get(u);
-                    acc[0][k].add(Sums<VEC>::pair(by, by), u);
-                }
-                m = c;
-                limit = kRefWeight * sum;
-            }
-        }
         first = false;
 #pragma unroll
         for (int s = 0; s < n; ++s) {
@@ -604,10 +558,11 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
                 sum += f0;
                 f1 = __shfl_xor_sync(kAll, f0, DL);
             } else if (MODE == kDQ) {
-                f1 = alpha[s];
-                f0 = f1 * (da[s] - m);
+                f1 = ex2(fmaf(x[s], P.c2, -own_lse));
+                f0 = f1 * da[s];
+                if (!valid) f0 = f1 = 0.f;
+                sum += f1;
                 dsum += f0;
-                draw = fmaf(f1, da[s], draw);
             } else {
                 const float p = sign * ex2(fmaf(x[s], P.c2, -st[s].x));
                 f1 = p + __shfl_xor_sync(kAll, p, DL);
@@ -736,8 +691,8 @@ struct Span {  // one cut row's slots, 0 .. n - 1
 };
 
 // A thread's sums over slots: CV columns of one map.  kFwd: s1, s2 the maps'
-// (maximum, sum), a, b their weighted sums; kDQ: s1 = (c, D'), s2 = (the sums of
-// alpha, of alpha da), a = A about c, b = B; kDKV: a, b.
+// (maximum, sum), a, b their weighted sums; kDQ: s1 = the sums of (alpha da,
+// alpha), a = A, b = B; kDKV: a, b.
 template <int MODE, int CV>
 struct FixSums {
     float2 s1, s2;
@@ -757,14 +712,8 @@ struct FixSums {
             s2 = make_float2(m2, fmaf(s2.y, f2, g2 * t2.y));
 #pragma unroll
             for (int v = 0; v < CV; ++v) a[v] = fmaf(a[v], f1, g1 * u[v]), b[v] = fmaf(b[v], f2, g2 * w[v]);
-        } else if (MODE == kDQ) {  // both about the mean da of the heavier
-            const float c = t2.x > s2.x ? t1.x + __fdividef(t1.y, t2.x) : s1.x + (s2.x > 0.f ? __fdividef(s1.y, s2.x) : 0.f);
-            const float p = s1.x - c, q = t1.x - c;
-            s1 = make_float2(c, fmaf(p, s2.x, s1.y) + fmaf(q, t2.x, t1.y));
-            s2.x += t2.x, s2.y += t2.y;
-#pragma unroll
-            for (int v = 0; v < CV; ++v) a[v] = fmaf(p, b[v], a[v]) + fmaf(q, w[v], u[v]), b[v] += w[v];
         } else {
+            if (MODE == kDQ) s1.x += t1.x, s1.y += t1.y;
 #pragma unroll
             for (int v = 0; v < CV; ++v) a[v] += u[v], b[v] += w[v];
         }
@@ -780,7 +729,7 @@ struct FixSums {
             F::unpack(F::load_written(p + c), u);
             F::unpack(F::load_written(p + c + P.H), w);
             if (MODE == kFwd) add(make_float2(p[q], p[q + h2]), make_float2(p[q + 1], p[q + 1 + h2]), u, w);
-            else if (MODE == kDQ) add(make_float2(p[q + map], p[q + map + 2 * h2]), make_float2(p[q + map + h2], p[q + map + 3 * h2]), u, w);
+            else if (MODE == kDQ) add(make_float2(p[q + map], p[q + map + h2]), s2, u, w);
             else add(s1, s2, u, w);
         }
     }
@@ -792,12 +741,8 @@ __device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c
     const float lam = P.lam[head];
     float f = 1.f, g = 0.f;
     if (MODE == kFwd) f = __fdividef(P.drop_scale, s.s1.y), g = -lam * __fdividef(P.drop_scale, s.s2.y);
-    if (MODE == kDQ) {
-        const float inv = __fdividef(1.f, s.s2.x);
-        s.s1.y *= inv;
-        f = (map ? -lam : 1.f) * P.scale * inv;
-        g = -s.s1.y * f;
-    }
+    const float inv = MODE == kDQ ? __fdividef(1.f, s.s1.y) : 0.f;
+    if (MODE == kDQ) f = (map ? -lam : 1.f) * P.scale * inv, g = -s.s1.x * inv * f;
     T *out = static_cast<T *>(P.out_a) + row * P.H + c;
     if (MODE != kDKV) {
 #pragma unroll
@@ -809,13 +754,13 @@ __device__ __forceinline__ void fix_store(const FixParams &P, int64_t row, int c
         const int64_t k = (row * P.heads + head) * 2 + map;
         const float2 m = MODE == kFwd && map ? s.s2 : s.s1;
         if (MODE == kFwd) P.lse_out[k] = (m.x + log2f(m.y)) * kLn2;
-        if (MODE == kDQ) P.stat[k] = make_float2(fmaf(s.s2.x - 1.f, kLog2e, P.lse[k] * kLog2e), __fdividef(s.s2.y, s.s2.x));
+        if (MODE == kDQ) P.stat[k] = make_float2(fmaf(s.s1.y - 1.f, kLog2e, P.lse[k] * kLog2e), s.s1.x * inv);
     }
 }
 
 template <typename T, int MODE, int CV>
 __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(const FixParams P) {
-    constexpr int kWords = 2 * CV + (MODE == kDKV ? 0 : 4);
+    constexpr int kWords = 2 * CV + (MODE == kFwd ? 4 : (MODE == kDQ ? 2 : 0));
     __shared__ float red[kWords][kFixThreads];
     follow_on();
     if (MODE == kDKV && P.lam_blocks > 0 && blockIdx.x == gridDim.x - 1) {
@@ -865,10 +810,8 @@ __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(
                 sum.add_slots(P, S, stripe, stripes, c, q, map);
 #pragma unroll
                 for (int v = 0; v < CV; ++v) red[v][threadIdx.x] = sum.a[v], red[CV + v][threadIdx.x] = sum.b[v];
-                if constexpr (MODE != kDKV) {
-                    red[2 * CV][threadIdx.x] = sum.s1.x, red[2 * CV + 1][threadIdx.x] = sum.s1.y;
-                    red[2 * CV + 2][threadIdx.x] = sum.s2.x, red[2 * CV + 3][threadIdx.x] = sum.s2.y;
-                }
+                if constexpr (MODE != kDKV) red[2 * CV][threadIdx.x] = sum.s1.x, red[2 * CV + 1][threadIdx.x] = sum.s1.y;
+                if constexpr (MODE == kFwd) red[2 * CV + 2][threadIdx.x] = sum.s2.x, red[2 * CV + 3][threadIdx.x] = sum.s2.y;
             }
             __syncthreads();
             if (stripe == 0 && c < P.H) {
@@ -878,10 +821,8 @@ __global__ void __launch_bounds__(kFixThreads, 1024 / kFixThreads) k_diff_fixup(
 #pragma unroll
                     for (int v = 0; v < CV; ++v) u[v] = red[v][i], w[v] = red[CV + v][i];
                     float2 t1 = sum.s1, t2 = sum.s2;
-                    if constexpr (MODE != kDKV) {
-                        t1 = make_float2(red[2 * CV][i], red[2 * CV + 1][i]);
-                        t2 = make_float2(red[2 * CV + 2][i], red[2 * CV + 3][i]);
-                    }
+                    if constexpr (MODE != kDKV) t1 = make_float2(red[2 * CV][i], red[2 * CV + 1][i]);
+                    if constexpr (MODE == kFwd) t2 = make_float2(red[2 * CV + 2][i], red[2 * CV + 3][i]);
                     sum.add(t1, t2, u, w);
                 }
                 fix_store<T, MODE, CV>(P, S.row, c, head, map, sum);
@@ -900,7 +841,7 @@ struct DiffLayout {
 };
 DiffLayout diff_layout(const ag_graph *g, int64_t H, int64_t heads) {
     DiffLayout L;
-    L.slot = (2 * H + 8 * heads + 3) / 4 * 4;
+    L.slot = (2 * H + 4 * heads + 3) / 4 * 4;
     const bool spans = g->dir[0].n_span > 0 || g->dir[1].n_span > 0;
     L.partial = 0;
     L.stat = align_up(spans ? size_t(2) * size_t(g->n_tiles) * size_t(L.slot) * 4 : 0);

@@ -21,12 +21,9 @@ Arithmetic, with U = 2^-24, B_e = scale sum |q k| of an edge and row r = dst_e:
   D      sum alpha da: Dd_r = sum alpha (rho_e + rho_r) |da| + sum alpha del_e
          + steps U sum alpha |da|.
   ds     scale alpha (da - D): scale alpha ((rho_e + rho_r)(|da| + |D|) + del_e + Dd_r).
-  dq     the sum of ds k, walked as sums of alpha (da - c) k and of alpha k: its
-         roundings are steps U times the sums of alpha (|da| + C) |k| and
-         (sum alpha |da| + C) alpha |k|, where |c| times the weight that it
-         serves is at most C: the largest |da| of the row's edges of at least
-         2^-10 of its largest weight, and 256 times the others' alpha |da| (c
-         has at least 1/256 of the weight that it serves).
+  dq     the sum of ds k, walked as sums of alpha da k and of alpha k: their
+         roundings are steps U times the sums of alpha |da| |k| and of
+         sum alpha |da| alpha |k|, twice.
   lse    sum alpha rho + steps U + 4 U |lse|.
   dK, dV recompute alpha from the rounded lse: 8 U (|lse| + 1) more.
   Outputs are rounded once to their type, half a step, or 2^-126 below its normal
@@ -76,8 +73,6 @@ def bounds(src, dst, N, Q, K, V, lam, scale, u, ref, dtype, dY=None):
     d = Q.shape[1] // (2 * h)
     E, dev = src.shape[0], Q.device
     total = lambda i, x: torch.zeros((N,) + x.shape[1:], dtype=torch.float64, device=dev).index_add_(0, i, x)
-    most = lambda x: torch.zeros((N,) + x.shape[1:], dtype=torch.float64, device=dev).scatter_reduce(
-        0, dst.view((E,) + (1,) * (x.dim() - 1)).expand_as(x), x, "amax")
     u = torch.ones(E, h, dtype=torch.float64, device=dev) if u is None else u
     q, k, v = Q.abs().view(N, h, 2, d), K.abs().view(N, h, 2, d), V.abs().view(N, h, 2 * d)
     half = torch.finfo(dtype).eps / 2
@@ -105,13 +100,10 @@ def bounds(src, dst, N, Q, K, V, lam, scale, u, ref, dtype, dY=None):
     ada = a * da
     A1 = total(dst, ada)                                                         # sum alpha |da|
     Dd = total(dst, ada * both + a * dele) + steps(cnt) * A1
-    amax = most(a)
-    heavy = a >= amax[dst] * 2.0 ** -10
-    C = most(torch.where(heavy, da, 0.0)) + 256 * total(dst, torch.where(heavy, 0.0, ada))
     own = a * (both * (da + D[dst]) + dele + Dd[dst])                            # ds / scale
     bq = total(dst, own[..., None] * k[src])
     ak = total(dst, a[..., None] * k[src])
-    round_q = 2 * steps(cnt)[..., None] * (total(dst, (a * (da + C[dst]))[..., None] * k[src]) + (A1 + C)[..., None] * ak)
+    round_q = 2 * steps(cnt)[..., None] * (total(dst, ada[..., None] * k[src]) + A1[..., None] * ak)
     out["dQ"] = ((bq + round_q) * (sc * al)[..., None]).view(N, -1) + half * ref["dQ"].abs() + TINY
     again = 8 * U * (torch.where(fin, lse, 0.0).abs() + 1)[dst]                  # alpha from the rounded lse
     full = a * (da + D[dst])

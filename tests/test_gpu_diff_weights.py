@@ -85,8 +85,18 @@ def test_equal_weights_and_one_large_value(agb, n):
     check(agb, np.arange(n), np.full(n, n), n + 1, torch.zeros_like(K), K, V, G, torch.full((1,), 0.5, device=DEV), 1.0)
 
 
+@pytest.mark.parametrize("offset", [10.0, 1e3])
+@pytest.mark.parametrize("n", [2, 5, 40, 3000])
+def test_values_that_lie_close_together(agb, n, offset):
+    # every da of a row is offset sum(dY) and a little: what cancels in dQ is as large as D itself
+    N = 300
+    rng = np.random.default_rng(n)
+    Q, K, V, G = (workloads.features(N, 32, torch.float32, k, DEV) for k in range(4))
+    check(agb, rng.integers(0, N, n), np.full(n, 7), N, Q, K, V + offset, G, torch.tensor([0.3, 0.7], device=DEV), 0.35)
+
+
 def test_one_edge_rows_have_no_gradient_of_scores(agb):
-    # a softmax of one edge is 1 whatever its score: dQ and dK are exactly 0 without dropout
+    # a softmax of one edge is 1 whatever its score: dQ is exactly 0
     N = 500
     src, dst = (torch.as_tensor(x).int().to(DEV) for x in (np.random.default_rng(0).integers(0, N, N), np.arange(N)))
     g = agb.ag_graph_lower(src, dst, N)
