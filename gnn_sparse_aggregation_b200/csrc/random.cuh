@@ -4,10 +4,10 @@
 // numbers: as easy as 1, 2, 3", SC 2011): ten rounds of two 32 x 32 -> 64-bit
 // products, the key advanced by two constants each round.  Element i of an
 // array uses word i % 4 of the block with counter (i / 4, offset) and key
-// seed, and is kept where that word is at least round(p 2^32).  The mask is a
-// function of (seed, offset, i) alone: the backward pass recomputes it, no
-// mask is stored, and any kernel that knows an element's index draws the same
-// bit whatever its schedule.
+// seed, and is kept where that word is at least round(p 2^32), or 2^32 - 1 where
+// that rounds to 2^32.  The mask is a function of (seed, offset, i) alone: the
+// backward pass recomputes it, no mask is stored, and any kernel that knows an
+// element's index draws the same bit whatever its schedule.
 #pragma once
 
 #include <math.h>

@@ -271,8 +271,11 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2 *red) {
     return v;
 }
 
-// 1 / (1 + 2^y), and of y = -x log2(e) the logistic function: off by at most
-// (|x| + 4) 2^-24, relative
+// 1 / (1 + 2^y), and of y = -x log2(e) the logistic function.  The constant and
+// the product round once each, which moves the exponential by 2 |x| 2^-24,
+// relative; the exponential and the division are off by 2 steps (2^-22) each, the
+// sum by half a step: (2 |x| + 9) 2^-24 down to x = -87.3.  Below, where it is
+// less than 2^-126, the result is 0.
 __device__ __forceinline__ float logistic2(float y) {
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));

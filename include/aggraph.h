@@ -342,7 +342,7 @@ AG_API int ag_attn_backward(const ag_graph *g, const void *Q, const void *K, con
  * Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011): element
  * i is kept where word i % 4 of the block with counter (i / 4, offset) and
  * key seed (both as pairs of 32-bit words, low first) is at least
- * round(p * 2^32), as an unsigned number:
+ * min(round(p * 2^32), 2^32 - 1), as an unsigned number:
  *   Y_i = X_i / (1 - p) where kept, else 0 (whatever X_i holds).
  * The mask is a function of (seed, offset, i) alone and is never stored: the
  * gradient is the same call on dY.  For features [N, H] i = n * H + h; for
@@ -468,7 +468,8 @@ AG_API int ag_diff_attn_backward(const ag_graph *g, const void *Q, const void *K
  *   Z = norm(X) * gamma2 + beta2
  * norm(x) = x / sqrt(mean(x^2) + eps) (AG_NORM_RMS), or the same of
  * x - mean(x) (AG_NORM_LAYER); act is the logistic function or x times it
- * (AG_ACT_SILU); drop is ag_dropout over [N, H].  Z is the norm of the fp32
+ * (AG_ACT_SILU), the logistic function being 0 below x = -87.3 (2^-126); drop is
+ * ag_dropout over [N, H].  Z is the norm of the fp32
  * sum, before it is rounded to X.  Every part may be left out (NULL): gamma
  * and scale are then 1, beta 0; without G no gate, without R the sum starts at
  * 0, without Z no second norm.  Without B (then no G and no X) Z is the norm
@@ -515,7 +516,8 @@ AG_API int ag_resnorm_fwd(const ag_resnorm *op, const void *R, const void *B, co
  *   dgamma1, dbeta1, dscale, dgamma2, dbeta2  device float [H], fully written
  *   scratch  device buffer, 256-byte aligned, of ag_resnorm_scratch_bytes(N, H)
  *            bytes; not needed without a column sum
- * The column sums are added in an order fixed by N and H (no atomics).
+ * The column sums are added in an order fixed by N, H, dtype and whether the
+ * addresses take vectors of four (no atomics).
  * Errors as ag_resnorm_fwd, and AG_ERR_WORKSPACE.
  */
 AG_API size_t ag_resnorm_scratch_bytes(int64_t N, int64_t H);
