@@ -89,3 +89,25 @@ def test_the_longest_joined_tiles(agb, E, tile, p):
     g = check(agb, src, dst, N, Q, K, V, G, torch.linspace(0.2, 0.8, 4, device=DEV), 1.0, drop, u)
     assert 4144 * tile <= g.stats["tiles"] * g.stats["tile_edges"] and tile > g.stats["tile_edges"]
     assert g.stats["max_degree_f"] > 20 * tile
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heads,d", [(64, 1), (65, 3), (100, 4), (130, 8), (256, 1), (256, 6), (200, 16)])
+def test_many_heads(agb, heads, d, dtype):
+    # more heads than a block of the walk has threads, and up to the most there may be; rows cut by tiles
+    rng = np.random.default_rng(heads)
+    N, E, p = 150, 900, 0.2
+    src, dst = rng.integers(0, N, E + 200), np.concatenate([rng.integers(0, N - 9, E), np.full(200, 5)])
+    Q, K, V, G = (workloads.features(N, 2 * heads * d, dtype, k, DEV) for k in range(4))
+    drop = dict(p=p, seed=11, offset=4)
+    check(agb, src, dst, N, Q, K, V, G, torch.linspace(0.1, 0.9, heads, device=DEV), d ** -0.5, drop,
+          lo.drop_factors((E + 200) * heads, p, 11, 4).reshape(-1, heads))
+
+
+@pytest.mark.parametrize("scale,lam", [(-0.5, 0.5), (0.0, 0.5), (0.3, 0.0), (0.3, -1.5), (0.3, 4.0)])
+def test_signs_of_the_scale_and_of_lambda(agb, scale, lam):
+    rng = np.random.default_rng(3)
+    N, E = 200, 2000
+    src, dst = rng.integers(0, N, E), rng.integers(0, N // 2, E)
+    Q, K, V, G = (workloads.features(N, 48, torch.float32, k, DEV) for k in range(4))
+    check(agb, src, dst, N, Q, K, V, G, torch.full((3,), lam, device=DEV), scale)
