@@ -48,18 +48,22 @@
 // partials that a fix-up kernel adds in tile order: results are bitwise
 // reproducible.
 //
-// What bounds it: warp instructions, then the L2's rate for gathered rows
-// (15.1 TB/s for random 256-byte rows).  Every node of 64 edges, H = 128 bf16,
-// 4 heads, 4.2 M edges (two rows, so 512 bytes, per edge): forward 194 us = 11
-// TB/s at 63 warp instructions per two edges, 256 us with dropout (Philox, 23
-// more), dQ 236 us, dK and dV 282 us.  On R-MAT-18 (the same sizes, dropout)
-// 370 / 400 / 420 us: 15 % of the time the last tiles run alone, and rows of a
-// few edges cost about 120 instructions each.  Measured and not taken: a row
-// split over the lane groups of a warp with sums across them at its end (660 us
-// forward); tiles cut finer than the schedule's (a warp's first loads and its
-// partials cost about 4 us: 1.41 ms in place of 1.19 for the step); 32 lanes of
-// 8 bytes per row in place of 16 of 16 (1.54 ms); four tiles per warp (2.2 ms);
-// 96 registers and 20 warps per SM in place of 128 and 16 (1.24 ms).
+// What bounds it where rows are even: warp instructions, then the L2's rate for
+// gathered rows (15.1 TB/s for random 256-byte rows).  Every node of 64 edges,
+// H = 128 bf16, 4 heads, 4.2 M edges (two rows, so 512 bytes, per edge):
+// forward 185-194 us = 11 TB/s at 63 warp instructions per two edges, 248-256
+// us with dropout (Philox, 23 more), dQ 218 us, dK and dV 274-282 us.  On
+// R-MAT-18 (the same sizes, dropout) 364 / 394 / 430 us, and neither bound is
+// reached: issue slots are busy 57 to 62 %, with 21 % of the warps active of
+// the 25 % that 128 registers allow, so the warps wait on their own last
+// results and on gathered rows; 15 % of the time the last tiles run alone, and
+// a row's end costs about 120 instructions, the other lane groups of its warp
+// masked.  Measured and not taken: a row split over the lane groups of a warp
+// with sums across them at its end (660 us forward); tiles cut finer than the
+// schedule's (a warp's first loads and its partials cost about 4 us: 1.41 ms in
+// place of 1.19 for the step); 32 lanes of 8 bytes per row in place of 16 of 16
+// (1.54 ms); four tiles per warp (2.2 ms); 96 registers and 20 warps per SM in
+// place of 128 and 16 (1.24 ms).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -21,10 +21,12 @@ constexpr int kSMs = 148;
 // ---------------------------------------------------------------------------- dropout
 
 // y_i = keep_i x_i / (1 - p).  A thread takes VEC (a multiple of 4) elements at
-// a time: VEC / 4 Philox blocks.  [2^20, 128] bf16: 121-124 us, 66-68 % of the
-// measured copy rate; the twenty wide products of a block hold the multiplier
-// 73 % busy, the exclusive-ors the other integer pipe 62 %.  Two vectors per
-// thread at a time measured 127-131 us.
+// a time: VEC / 4 Philox blocks.  [2^20, 128] bf16: 119-124 us, 66-69 % of the
+// measured copy rate.  Bound by the integer pipes: with 92 % of the warps active
+// the most frequent stall is on a busy pipe (the exclusive-ors, compares and
+// moves hold theirs 66 % busy, the twenty wide products a block theirs 39 %, where
+// such a product takes more than one slot).  Two vectors per thread at a time
+// measured 127-131 us.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_dropout(const T *__restrict__ x, T *__restrict__ y, int64_t n, const Drop drop) {
     using F = Frag<T, VEC>;
@@ -230,11 +232,18 @@ void dispatch_rotary(RotaryParams &P, bool half, uintptr_t addresses, cudaStream
 // forward:  X = R + scale * drop(act(G) * (norm(B) * gamma1 + beta1)),  Z = norm(X) * gamma2 + beta2
 // norm: x / sqrt(mean(x^2) + eps), or with the mean subtracted first.  One pass;
 // a row stays in registers, its statistics are sums over the lanes that hold it.
-// Bound by HBM and, with dropout, by instructions: forward [2^20, 128] bf16,
-// LAYER, SiLU, p = 0.1: 280-296 us, 69-73 % of the measured copy rate at 49
-// instructions an element (556 us with vectors loaded value by value); backward
-// [156323, 256] fp32, p = 0.1: 234-248 us, 79-84 % (352 us with 64 threads and
-// eight barriers a row in place of a warp).
+// Forward [2^20, 128] bf16, LAYER, SiLU: 258 us, with p = 0.1 275-296 us, 69-75 %
+// of the measured copy rate at 47 instructions an element (556 us with vectors
+// loaded value by value): no pipe is full (issue slots 63 %, DRAM 56 % of nominal),
+// but 96 registers, 32 of them the four vectors and 12 the next row, leave 28 % of
+// the warps.  Backward [156323, 256] fp32, p = 0.1: 232-248 us, 79-84 %, HBM (352
+// us with 64 threads and eight barriers a row in place of a warp).  Backward in
+// bf16 takes four features a thread and fp32 arithmetic value by value, and is
+// bound by instructions: [2^20, 128], p = 0.1: 863 us against 328 for the bytes.
+// Rows of more than 64 vectors of four span several warps and wait at block
+// barriers: 2^26 elements in rows of 512 to 8192, p = 0.1, run at 33 to 92 % of the
+// copy rate forward and 42 to 70 % backward in fp32, 26 to 63 % and 23 to 43 % in
+// bf16 (the least from 4096 on).
 struct NormParams {
     const void *R, *B, *G, *X, *dX, *dZ;      // inputs (absent: null)
     void *oX, *oZ, *dR, *dB, *dG;             // outputs (absent: null)
@@ -675,7 +684,8 @@ void launch_norm(const NormParams &P, int *blocks, cudaStream_t st) {
 }
 // Threads per row: the power of two that covers the row's n vectors.  Up to
 // 64 vectors of four a row stays in a warp (two vectors a thread: no block
-// barrier in the row sums).
+// barrier in the row sums; [156323, 256] fp32 backward 352 -> 234 us).  Wider rows
+// in a warp, with more vectors a thread, are not measured.
 template <typename T, int VEC, bool BACK>
 void dispatch_norm(const NormParams &P, int *blocks, cudaStream_t st) {
     const int n = (P.H + VEC - 1) / VEC;
