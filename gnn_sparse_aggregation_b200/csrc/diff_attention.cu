@@ -535,8 +535,9 @@ __global__ void __launch_bounds__(kWarps * 32, NV <= 2 ? kMinBlocks : 1) k_diff_
                 top = fmaxf(top, x[s]);
             }
             if (first) m = fmaxf(x[0], -3.402823466e38f);  // never -inf: exp2(-inf - m) is 0
-            if (__any_sync(kAll, top > m + kSlack)) {
-                top = fmaxf(m, top);
+            const bool beyond = top > m + kSlack;
+            if (__any_sync(kAll, beyond)) {
+                top = beyond ? top : m;  // (the warp's other rows keep their bits)
                 const float f = ex2(m - top);
                 const float g = __shfl_xor_sync(kAll, f, DL);
                 sum *= f;

@@ -111,3 +111,21 @@ def test_signs_of_the_scale_and_of_lambda(agb, scale, lam):
     src, dst = rng.integers(0, N, E), rng.integers(0, N // 2, E)
     Q, K, V, G = (workloads.features(N, 48, torch.float32, k, DEV) for k in range(4))
     check(agb, src, dst, N, Q, K, V, G, torch.full((3,), lam, device=DEV), scale)
+
+
+@pytest.mark.parametrize("heads,d,dtype", [(1, 4, torch.float32), (2, 8, torch.float32), (4, 16, torch.bfloat16), (3, 5, torch.bfloat16)])
+def test_rows_do_not_depend_on_other_rows(agb, heads, d, dtype):
+    # rows of rising scores of 100, and of infinite ones, beside rows of small scores: these keep their bits
+    rng = np.random.default_rng(6)
+    N, E = 40_000, 400_000
+    src, dst = (torch.as_tensor(rng.integers(0, N, E).astype(np.int32)).to(DEV) for _ in range(2))
+    g = agb.ag_graph_lower(src, dst, N)
+    Q, K, V = (workloads.features(N, 2 * heads * d, dtype, k, DEV) for k in range(3))
+    lam = torch.linspace(0.3, 0.7, heads, device=DEV)
+    want = agb.ag_diff_attn_fwd(g, Q, K, V, lam, d ** -0.5)
+    rest = torch.arange(N, device=DEV) % 3 != 0
+    for factor in (50.0, float("inf")):
+        got = agb.ag_diff_attn_fwd(g, torch.where(rest[:, None], Q, Q * factor), K, V, lam, d ** -0.5)
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a[rest], b[rest])
